@@ -10,14 +10,22 @@ GPU is present the calls raise.
 Raw ABI (same names and argument order as ``include/fa.h``; pointers are ints):
     fa_fwd, fa_bwd, fa_bwd_preprocess, fa_bwd_main, fa_bwd_postprocess,
     fa_bwd_workspace_bytes, fa_bwd_noalloc, fa_fwd_dropout, fa_bwd_dropout, fa_fwd_fp8, fa_fwd_fp8_per_head, fa_attn_merge, fa_accumulate,
-    fa_decode,
-    fa_decode_workspace_bytes, fa_check_device_status, fa_set_watchdog_ns, fa_watchdog_selftest, fa_status_string, fa_version
+    fa_decode, fa_decode_workspace_bytes,
+    fa_rope_table, fa_qk_norm_rope, fa_qk_norm_rope_bwd, fa_qk_norm_rope_bwd_workspace_bytes, fa_cache_bytes, fa_cache_append,
+    fa_cache_gather, fa_decode_paged, fa_decode_paged_workspace_bytes,
+    fa_check_device_status, fa_set_watchdog_ns, fa_watchdog_selftest, fa_status_string, fa_version
 Torch wrappers:
     attention_forward(q, k, v, ...)          -> (o, lse)
     attention_backward(q, k, v, o, lse, do, ...) -> (dq, dk, dv)
     attention_decode(q, k, v, ...)           -> (o, lse)   one query per sequence over a K/V cache
     attention_forward_fp8(q8, k8, v8, descales, ...) -> (o bf16, lse)   e4m3 inputs
     attention_merge(acc_o, acc_lse, part_o, part_lse, ...)   merge a partial (O, LSE) into a running result
+    attention_rope_table(rows, rot_dim, base)    -> (cos, sin)   the angles of the rotation by position
+    attention_qk_norm_rope(q, k, cos, sin, positions, ...)   -> (q_out, k_out)   per-head norm and rotation
+    attention_qk_norm_rope_backward(dq_out, dk_out, ...)     -> (dq, dk, dwq, dwk)
+    attention_cache_append(k, v, k_cache, v_cache, ...)      new keys and values into a paged cache (16 or 4 bits)
+    attention_cache_gather(k_cache, v_cache, ...)            -> (k, v)   rows of a paged cache, packed
+    attention_decode_paged(q, k_cache, v_cache, ...)         -> (o, lse)   new queries over a paged cache
 Ring (context-parallel) attention over a process group: ``exact_io_aware_90_b200.ring``.
 """
 
@@ -34,10 +42,16 @@ __all__ = [
     "fa_fwd", "fa_bwd", "fa_bwd_preprocess", "fa_bwd_main", "fa_bwd_postprocess", "fa_bwd_workspace_bytes",
     "fa_bwd_noalloc", "FA_NOALLOC_SCRATCH_BYTES", "fa_fwd_dropout", "fa_bwd_dropout", "fa_fwd_fp8", "fa_fwd_fp8_per_head", "fa_attn_merge", "fa_accumulate", "fa_decode", "fa_decode_workspace_bytes", "fa_check_device_status", "fa_set_watchdog_ns", "fa_watchdog_selftest", "fa_status_string", "fa_version",
     "attention_forward", "attention_backward", "attention_decode", "attention_forward_fp8", "attention_merge", "dtype_code",
+    "FA_CACHE_16BIT", "FA_CACHE_INT4", "fa_rope_table", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
+    "fa_qk_norm_rope_bwd_workspace_bytes", "fa_cache_bytes", "fa_cache_append", "fa_cache_gather", "fa_decode_paged",
+    "fa_decode_paged_workspace_bytes",
+    "attention_rope_table", "attention_qk_norm_rope", "attention_qk_norm_rope_backward", "attention_cache_append",
+    "attention_cache_gather", "attention_decode_paged",
 ]
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = 0, 1, 2, 3, 4
 FA_BF16, FA_FP16 = 0, 1
+FA_CACHE_16BIT, FA_CACHE_INT4 = 0, 1
 FA_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # include/fa.h
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa_b200.so")
@@ -56,6 +70,7 @@ def _load() -> ctypes.CDLL:
             "(nvcc, sm_100a). There is no fallback implementation.")
     L = ctypes.CDLL(LIB_PATH)
     P, I, F, S, U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_uint64
+    LL = ctypes.c_longlong
     sig = {
         "fa_fwd": (I, [P, P, P, P, P, I, I, I, I, F, I, P, I, I, P]),
         "fa_bwd_workspace_bytes": (S, [I, I, I]),
@@ -74,6 +89,15 @@ def _load() -> ctypes.CDLL:
         "fa_accumulate": (I, [P, P, P, ctypes.c_longlong, I, I, P]),
         "fa_decode_workspace_bytes": (S, [I, I, I, I]),
         "fa_decode": (I, [P, P, P, P, P, I, I, I, I, F, P, I, I, P, S, P]),
+        "fa_rope_table": (I, [P, P, I, I, ctypes.c_double, P]),
+        "fa_qk_norm_rope": (I, [P] * 9 + [I] * 4 + [LL] * 4 + [I, I, I, P, I, F, I, P]),
+        "fa_qk_norm_rope_bwd_workspace_bytes": (S, [I]),
+        "fa_qk_norm_rope_bwd": (I, [P] * 13 + [I] * 4 + [LL] * 6 + [I, I, I, P, I, F, I, P, S, P]),
+        "fa_cache_bytes": (S, [I, I, I, I, I]),
+        "fa_cache_append": (I, [P] * 14 + [I] * 5 + [LL] * 4 + [I] * 6 + [P, I, F, I, I, P]),
+        "fa_cache_gather": (I, [P] * 7 + [I] * 9 + [P]),
+        "fa_decode_paged_workspace_bytes": (S, [I] * 6),
+        "fa_decode_paged": (I, [P] * 7 + [I] * 6 + [F] + [I] * 5 + [P, S, P]),
         "fa_check_device_status": (I, [P]),
         "fa_set_watchdog_ns": (None, [U64]),
         "fa_watchdog_selftest": (I, [U64, P]),
@@ -178,6 +202,58 @@ def fa_decode(q, k, v, o, lse, B, H, Nk, d, scale, cu_seqlens_k, total_keys, dty
               stream) -> int:
     return lib.fa_decode(q, k, v, o, lse, B, H, Nk, d, scale, cu_seqlens_k, total_keys, dtype, workspace,
                          workspace_bytes, stream)
+
+
+def fa_rope_table(cos_t, sin_t, table_rows, rot_dim, base, stream) -> int:
+    return lib.fa_rope_table(cos_t, sin_t, table_rows, rot_dim, base, stream)
+
+
+def fa_qk_norm_rope(q, k, q_out, k_out, wq, wk, cos_t, sin_t, positions, T, Hq, Hk, d, q_stride, k_stride, q_out_stride,
+                    k_out_stride, rot_dim, table_rows, axes, sections, interleaved, eps, dtype, stream) -> int:
+    return lib.fa_qk_norm_rope(q, k, q_out, k_out, wq, wk, cos_t, sin_t, positions, T, Hq, Hk, d, q_stride, k_stride,
+                               q_out_stride, k_out_stride, rot_dim, table_rows, axes, sections, interleaved, eps, dtype,
+                               stream)
+
+
+def fa_qk_norm_rope_bwd_workspace_bytes(d) -> int:
+    return lib.fa_qk_norm_rope_bwd_workspace_bytes(d)
+
+
+def fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, cos_t, sin_t, positions, dq, dk, dwq, dwk, T, Hq, Hk, d,
+                        dq_out_stride, dk_out_stride, q_stride, k_stride, dq_stride, dk_stride, rot_dim, table_rows, axes,
+                        sections, interleaved, eps, dtype, workspace, workspace_bytes, stream) -> int:
+    return lib.fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, cos_t, sin_t, positions, dq, dk, dwq, dwk, T, Hq, Hk, d,
+                                   dq_out_stride, dk_out_stride, q_stride, k_stride, dq_stride, dk_stride, rot_dim,
+                                   table_rows, axes, sections, interleaved, eps, dtype, workspace, workspace_bytes, stream)
+
+
+def fa_cache_bytes(num_pages, page_size, Hk, d, cache_format) -> int:
+    return lib.fa_cache_bytes(num_pages, page_size, Hk, d, cache_format)
+
+
+def fa_cache_append(q, k, v, q_out, k_cache, v_cache, wq, wk, cos_t, sin_t, positions, page_table, seqlens_k, cu_seqlens, B, T,
+                    Hq, Hk, d, q_stride, k_stride, v_stride, q_out_stride, page_size, num_pages, max_pages, rot_dim,
+                    table_rows, axes, sections, interleaved, eps, dtype, cache_format, stream) -> int:
+    return lib.fa_cache_append(q, k, v, q_out, k_cache, v_cache, wq, wk, cos_t, sin_t, positions, page_table, seqlens_k,
+                               cu_seqlens, B, T, Hq, Hk, d, q_stride, k_stride, v_stride, q_out_stride, page_size,
+                               num_pages, max_pages, rot_dim, table_rows, axes, sections, interleaved, eps, dtype,
+                               cache_format, stream)
+
+
+def fa_cache_gather(k_cache, v_cache, k, v, page_table, cu_seqlens_k, starts, B, total_keys, Hk, d, page_size, num_pages,
+                    max_pages, dtype, cache_format, stream) -> int:
+    return lib.fa_cache_gather(k_cache, v_cache, k, v, page_table, cu_seqlens_k, starts, B, total_keys, Hk, d, page_size,
+                               num_pages, max_pages, dtype, cache_format, stream)
+
+
+def fa_decode_paged_workspace_bytes(B, Nq, H, Hk, Nk, d) -> int:
+    return lib.fa_decode_paged_workspace_bytes(B, Nq, H, Hk, Nk, d)
+
+
+def fa_decode_paged(q, k_cache, v_cache, o, lse, page_table, seqlens_k, B, Nq, H, Hk, Nk, d, scale, page_size, num_pages,
+                    max_pages, dtype, cache_format, workspace, workspace_bytes, stream) -> int:
+    return lib.fa_decode_paged(q, k_cache, v_cache, o, lse, page_table, seqlens_k, B, Nq, H, Hk, Nk, d, scale, page_size,
+                               num_pages, max_pages, dtype, cache_format, workspace, workspace_bytes, stream)
 
 
 def fa_check_device_status(stream) -> int:
@@ -410,3 +486,18 @@ def attention_decode(q, k, v, scale: Optional[float] = None, cu_seqlens_k=None, 
     if st != FA_OK:
         raise FAError(st, "fa_decode")
     return out, lse
+
+
+
+# The wrappers of paged.py need torch at import; they are loaded on first use, so that the raw ABI does not.
+_PAGED = ("attention_rope_table", "attention_qk_norm_rope", "attention_qk_norm_rope_backward", "attention_cache_append",
+          "attention_cache_gather", "attention_decode_paged")
+
+
+def __getattr__(name):
+    if name in _PAGED:
+        from . import paged
+        for n in _PAGED:
+            globals()[n] = getattr(paged, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

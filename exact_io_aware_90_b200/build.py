@@ -17,8 +17,9 @@ ROOT = os.path.dirname(HERE)
 LIB_NAME = "libfa_b200.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["libfa_b200.cu"]
-DEPS = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu", "fa_merge.cu", "fa_noalloc.cu"]
-HEADERS = ["fa_internal.h", "sm100.cuh", os.path.join("..", "..", "include", "fa.h")]
+DEPS = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu", "fa_merge.cu", "fa_noalloc.cu", "fa_rope.cu",
+        "fa_cache.cu", "fa_paged.cu", "fa_paged_api.cu"]
+HEADERS = ["fa_internal.h", "sm100.cuh", "rope.cuh", "paged.cuh", os.path.join("..", "..", "include", "fa.h")]
 
 
 def nvcc_path() -> str:

@@ -6,3 +6,7 @@
 #include "fa_decode.cu"
 #include "fa_merge.cu"
 #include "fa_noalloc.cu"
+#include "fa_rope.cu"
+#include "fa_cache.cu"
+#include "fa_paged.cu"
+#include "fa_paged_api.cu"

@@ -1,0 +1,84 @@
+// paged.cuh — the paged key/value cache: addresses of its rows, the 4-bit row format, and the search for
+// the sequence that owns a token.
+//
+// A cache is pages of page_size tokens; the keys and the values of one (page, head) are one contiguous
+// block, so that a tile of a page is one contiguous copy.
+//   16 bits  page_size rows of d elements
+//   4 bits   page_size rows of d/2 bytes of numbers, then page_size rows of d/32 (scale, min) pairs of
+//            fp16, one pair for each 32 features of the row: the value is number·scale + min
+// The order of the numbers in a row is the order in which the decode kernel's lanes hold them (W = d/32):
+//   key    feature 32w + 8t + n (t < 4, n < 8): nibble n of 32-bit word t·W + w
+//   value  feature 32w + 4g + n (g < 8, n < 4): nibble n of 16-bit word g·W + w
+#pragma once
+
+#include "fa_internal.h"
+#include "sm100.cuh"
+
+namespace fa {
+
+// Bytes of one (page, head) block.
+__host__ __device__ constexpr size_t cache_block_bytes(int d, int page_size, bool q4) {
+  return q4 ? (size_t)page_size * (d / 2 + d / 8) : (size_t)page_size * d * 2;
+}
+
+// The sequence that owns token t: the number of entries of cu[1..B] that are <= t (B when none owns it).
+// All 32 lanes call it; each step looks at 32 evenly spaced entries.
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int B, int t) {
+  const int lane = (int)lane_id();
+  int lo = 0, n = B;
+  while (n > 32) {
+    const int step = (n + 31) / 32;
+    const int i = (lane + 1) * step - 1;
+    const bool below = i < n && __ldg(cu + 1 + lo + i) <= t;
+    const int c = __popc(__ballot_sync(0xffffffffu, below));
+    lo += c * step;
+    n = min(step, n - c * step);
+    if (n <= 0) return lo;
+  }
+  const bool below = lane < n && __ldg(cu + 1 + lo + lane) <= t;
+  return lo + __popc(__ballot_sync(0xffffffffu, below));
+}
+
+// Page of position `at` of sequence b, or -1 with the status recorded (one lane's worth) when the
+// position or the table's entry is out of range.
+__device__ __forceinline__ int page_of(const PagedArgs& p, int b, int at, int& slot) {
+  int page = -1;
+  slot = 0;
+  if (at >= 0 && at / p.page_size < p.max_pages) {
+    const int i = at / p.page_size;
+    slot = at - i * p.page_size;
+    page = __ldg(p.page_table + (size_t)b * p.max_pages + i);
+    if (page >= p.num_pages) page = -1;
+  }
+  if (page < 0) {
+    if (lane_id() == 0) record_status(1);
+    return -1;
+  }
+  return page;
+}
+
+// 16 consecutive values of a row (half of a group of 32; the other half is in the neighbouring lane, lane
+// xor 1) as 4-bit numbers, and the group's scale and minimum as fp16 bits (scale in the low half).  The
+// minimum is rounded to fp16 first and the numbers are taken from it, so the rounding adds no error of
+// its own; the division is IEEE, so equal inputs give equal numbers wherever they are computed.
+__device__ __forceinline__ uint32_t quantise16(const float (&x)[16], uint32_t (&n)[16]) {
+  float lo = x[0], hi = x[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) {
+    lo = fminf(lo, x[i]);
+    hi = fmaxf(hi, x[i]);
+  }
+  lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+  hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+  const __half hmin = __float2half_rn(fminf(fmaxf(lo, -65504.f), 65504.f));
+  const __half hsc = __float2half_rn(fminf(__fdiv_rn(hi - lo, 15.f), 65504.f));
+  const float mn = __half2float(hmin), sc = __half2float(hsc);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float v = sc > 0.f ? rintf(__fdiv_rn(x[i] - mn, sc)) : 0.f;
+    n[i] = (uint32_t)fminf(fmaxf(v, 0.f), 15.f);
+  }
+  return (uint32_t)__half_as_ushort(hsc) | ((uint32_t)__half_as_ushort(hmin) << 16);
+}
+
+}  // namespace fa

@@ -351,6 +351,157 @@ int fa_decode(const void* q, const void* k, const void* v, void* o, float* lse,
               fa_stream_t stream);
 
 /*
+ * Queries and keys made ready for the attention: the RMS norm of each head
+ * and the rotation by position, in one pass in front of fa_fwd.
+ *   norm      n_f = x_f · w_f / √(mean_f x_f² + eps) over the d features of a
+ *             head; wq and wk (dtype [d], shared by the heads) both NULL: no norm
+ *   rotation  the first rot_dim features form rot_dim/2 pairs (a, b), turned to
+ *             (a·cos − b·sin, b·cos + a·sin); the others pass.  Pair i is the
+ *             features (i, i + rot_dim/2), or (2i, 2i + 1) with interleaved = 1.
+ * Angles.  cos_t and sin_t are fp32 [table_rows, rot_dim/2], 16-byte aligned:
+ *   entry (p, i) belongs to position p and pair i (any frequencies; those of
+ *   fa_rope_table are p·base^(−2i/rot_dim)).  positions is a device int32
+ *   [axes, T].  axes = 1: pair i of token t takes row positions[t].  axes 2 to 4
+ *   (time, height and width of images and video): the pairs are split in order
+ *   into `sections` (host int[axes], multiples of 4 that add up to rot_dim/2),
+ *   and those of section a take row positions[a·T + t].  A position outside
+ *   [0, table_rows) records FA_ERR_INVALID_ARG; its token is skipped.
+ *   q, k          in   [T, Hq, d] and [T, Hk, d] dtype
+ *   q_out, k_out  out  the same shapes; each may be its own input (same pointer
+ *                 and stride), and may not overlap anything else
+ *   *_stride      elements between two tokens of an array: at least H·d, a
+ *                 multiple of 8 (slices of one projection's output are fine)
+ *   rot_dim       multiple of 16, at most d;  eps finite, > 0 (with norm)
+ * Hq and Hk are independent.  Arithmetic in fp32, rounded once at the end.
+ * Bound by memory: q and k are read once and written once.
+ */
+int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const void* wq, const void* wk,
+                    const float* cos_t, const float* sin_t, const int32_t* positions, int T, int Hq, int Hk, int d,
+                    long long q_stride, long long k_stride, long long q_out_stride, long long k_out_stride,
+                    int rot_dim, int table_rows, int axes, const int* sections, int interleaved, float eps, int dtype,
+                    fa_stream_t stream);
+
+/*
+ * Gradients of fa_qk_norm_rope.  With g the gradient of the output turned back
+ * by the angle, r = 1/√(mean x² + eps) and n = x·r:
+ *   dx = r·(g∘w − n·mean(g∘w∘n)),   dw = Σ over tokens and heads of g∘n
+ * (no norm: dx = g).
+ *   dq_out, dk_out  in   gradients of q_out, k_out (dq and dk of fa_bwd)
+ *   q, k            in   the forward's inputs (not read without norm; may be NULL)
+ *   dq, dk          out  dtype; each may be its own dq_out / dk_out
+ *   dwq, dwk        out  fp32 [d] (not written without norm; may be NULL).  The
+ *                   sums are taken in a fixed order: equal calls give equal bits.
+ *                   Tokens that are skipped add nothing.
+ *   workspace       at least fa_qk_norm_rope_bwd_workspace_bytes(d) bytes, 256-byte
+ *                   aligned, contents irrelevant (needed with norm only)
+ */
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int d);
+int fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, const void* wq,
+                        const void* wk, const float* cos_t, const float* sin_t, const int32_t* positions, void* dq,
+                        void* dk, float* dwq, float* dwk, int T, int Hq, int Hk, int d, long long dq_out_stride,
+                        long long dk_out_stride, long long q_stride, long long k_stride, long long dq_stride,
+                        long long dk_stride, int rot_dim, int table_rows, int axes, const int* sections,
+                        int interleaved, float eps, int dtype, void* workspace, size_t workspace_bytes,
+                        fa_stream_t stream);
+
+/*
+ * The table of angles: cos_t and sin_t [table_rows, rot_dim/2] of
+ * p·base^(−2i/rot_dim), computed in 64 bits and rounded to fp32.  base > 1.
+ */
+int fa_rope_table(float* cos_t, float* sin_t, int table_rows, int rot_dim, double base, fa_stream_t stream);
+
+/*
+ * Paged key/value cache
+ * ---------------------
+ * k_cache and v_cache are num_pages pages of page_size tokens each; page_table
+ * is a device int32 [B, max_pages]: position j of sequence b lies in page
+ * page_table[b, j / page_size], slot j % page_size.  Entries behind a sequence's
+ * last page are not read.  seqlens_k is a device int32 [B] of key counts.
+ * page_size: a multiple of 16 (FA_ERR_UNSUPPORTED otherwise), max_pages·page_size
+ * at most 2^30; the caches 16-byte aligned, fa_cache_bytes(...) bytes each.
+ * Rows are [num_pages, Hk, page_size]; the rows of one page and head are one block:
+ *   FA_CACHE_16BIT  page_size rows of d elements of the dtype.
+ *   FA_CACHE_INT4   page_size rows of d/2 bytes, then page_size rows of d/32 pairs
+ *                   (scale, min) of fp16.  Each 32 features share a pair; a 4-bit
+ *                   number n stands for n·scale + min.  With W = d/32,
+ *                   feature 32w + 8t + n (t < 4, n < 8) of a key is nibble n of the
+ *                   row's 32-bit word t·W + w; feature 32w + 4g + n (g < 8, n < 4) of
+ *                   a value is nibble n of its 16-bit word g·W + w; the pair of
+ *                   group w is the w-th.
+ * A 4-bit row is made from the row rounded to the dtype: min = the least of the 32
+ * values in fp16, scale = (largest − least)/15 in fp16 (both kept within ±65504),
+ * n = (value − min)/scale rounded to nearest even and kept within 0..15 (0 when
+ * scale is 0).
+ * What the device finds out of range (lengths, offsets, pages, positions) records
+ * FA_ERR_INVALID_ARG in the device status word and is skipped; nothing outside the
+ * caches is touched.
+ */
+typedef enum { FA_CACHE_16BIT = 0, FA_CACHE_INT4 = 1 } fa_cache_format;
+
+/* Bytes of one cache (keys or values).  0 for invalid sizes. */
+size_t fa_cache_bytes(int num_pages, int page_size, int Hk, int d, int cache_format);
+
+/*
+ * Appends new keys and values to a paged cache, with the norm and rotation of
+ * fa_qk_norm_rope applied to the keys on the way, and (q given) to the queries
+ * of the same tokens, which go to q_out: one launch prepares a decoding step.
+ *   k, v         in   [T, Hk, d] dtype, token strides as in fa_qk_norm_rope
+ *   q, q_out     [T, Hq, d], or NULL with Hq = 0; q_out may be q
+ *   cu_seqlens   device int32 [B+1]: the new tokens of sequence b are rows
+ *                [cu_seqlens[b], cu_seqlens[b+1]); NULL: T/B tokens each
+ *   seqlens_k    key counts AFTER the append: the n new tokens of sequence b
+ *                become positions seqlens_k[b] − n .. seqlens_k[b] − 1
+ *   wq, wk       norm weights, both or neither (wk alone without q)
+ *   positions    int32 [axes, T]; NULL (axes = 1): the position in the sequence
+ *   cos_t, sin_t both NULL: no rotation
+ * Rows behind the last sequence are left as they are, and so are q_out's.  Two
+ * tokens with the same page and slot are written in an undefined order.
+ */
+int fa_cache_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache, void* v_cache,
+                    const void* wq, const void* wk, const float* cos_t, const float* sin_t, const int32_t* positions,
+                    const int32_t* page_table, const int32_t* seqlens_k, const int32_t* cu_seqlens, int B, int T, int Hq,
+                    int Hk, int d, long long q_stride, long long k_stride, long long v_stride, long long q_out_stride,
+                    int page_size, int num_pages, int max_pages, int rot_dim, int table_rows, int axes,
+                    const int* sections, int interleaved, float eps, int dtype, int cache_format, fa_stream_t stream);
+
+/*
+ * Reads rows of a paged cache back into packed k, v [total_keys, Hk, d] of the
+ * dtype (what fa_fwd and fa_decode read): row cu_seqlens_k[b] + i is position
+ * starts[b] + i of sequence b (starts NULL: 0; cu_seqlens_k NULL: total_keys/B
+ * rows each).  4-bit rows come as n·scale + min, rounded once.  Rows that belong
+ * to no sequence are left as they are.
+ */
+int fa_cache_gather(const void* k_cache, const void* v_cache, void* k, void* v, const int32_t* page_table,
+                    const int32_t* cu_seqlens_k, const int32_t* starts, int B, int total_keys, int Hk, int d,
+                    int page_size, int num_pages, int max_pages, int dtype, int cache_format, fa_stream_t stream);
+
+/*
+ * Decode over a paged cache: the last Nq tokens of each sequence (Nq = 1: token
+ * by token; more: drafted tokens checked at once) attend to the sequence's keys.
+ *   q, o         [B, Nq, H, d] dtype; query head h reads key head h / (H/Hk)
+ *   lse          fp32 [B, Nq, H]
+ *   seqlens_k    key counts, the new tokens' keys included (as after
+ *                fa_cache_append), each at most Nk; query i of sequence b sees
+ *                the keys up to position seqlens_k[b] − Nq + i, and one that sees
+ *                none gets o = 0, lse = −inf
+ *   Nk           bound of every key count (it sizes the launch and the workspace);
+ *                lengths above max_pages·page_size are out of range too
+ * H a multiple of Hk.  Keys and values that a query does not see may hold anything
+ * (infinities, NaN); an infinity or NaN in a value that it sees makes that feature
+ * of o infinite or NaN.
+ * The scores and sums are fp32; P carries two 16-bit parts into the product with
+ * V (4-bit cache: one fp16 part of P times the value's scale).  The workspace
+ * holds the parts of chunks of keys, as in fa_decode; a 256-byte aligned buffer of
+ * fa_decode_paged_workspace_bytes(...) bytes.  A sequence whose length is out of
+ * range is skipped, its rows of o and lse left as they are.
+ */
+size_t fa_decode_paged_workspace_bytes(int B, int Nq, int H, int Hk, int Nk, int d);
+int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                    const int32_t* page_table, const int32_t* seqlens_k, int B, int Nq, int H, int Hk, int Nk, int d,
+                    float scale, int page_size, int num_pages, int max_pages, int dtype, int cache_format,
+                    void* workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
  * Synchronises `stream`, returns the device status word (FA_OK, or the first
  * FA_ERR_TIMEOUT / FA_ERR_INVALID_ARG a kernel recorded since the last call)
  * and clears it.  Returns FA_ERR_CUDA if the synchronisation itself failed.

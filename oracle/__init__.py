@@ -36,6 +36,17 @@ Parity status of each function (what pins it; see ``tests/test_oracle.py``):
                           pinned: p = 0 equals the plain oracle, unbiased over
                           seeds, finite differences with the mask fixed, the
                           D identity.
+* rope_table, qk_norm_rope, qk_norm_rope_backward
+                          pinned: closed forms (position 0, a quarter turn, complex products), unit mean
+                          square after the norm, lengths kept by the rotation, finite differences.
+* four_bit_rows, four_bit_pack, four_bit_unpack, page_slots, cache_rows
+                          pinned: the layout's formula element by element, the round trip, the error bound.
+* decode_paged            pinned: equals decode_forward with one query, and the last rows of causal
+                          attention_forward with several.
 """
+from . import attention as _attention
+from . import paged as _paged
 from .attention import *  # noqa: F401,F403
-from .attention import __all__  # noqa: F401
+from .paged import *  # noqa: F401,F403
+
+__all__ = _attention.__all__ + _paged.__all__
