@@ -58,6 +58,7 @@ static int set_paged(PagedArgs* p, const void* k_cache, const void* v_cache, con
   if (format != FA_CACHE_16BIT && format != FA_CACHE_INT4) return FA_ERR_INVALID_ARG;
   if ((page_size & 15) != 0 || page_size > (1 << 20)) return FA_ERR_UNSUPPORTED;
   if ((long long)max_pages * page_size > (1LL << 30)) return FA_ERR_UNSUPPORTED;
+  if ((long long)Hk * page_size > (1LL << 31) / (2 * d)) return FA_ERR_UNSUPPORTED;  // a page's bytes in 32 bits
   if (Hk > 65535 || B > (1 << 24)) return FA_ERR_UNSUPPORTED;
   p->k_cache = const_cast<void*>(k_cache);
   p->v_cache = const_cast<void*>(v_cache);
@@ -76,11 +77,11 @@ static int set_paged(PagedArgs* p, const void* k_cache, const void* v_cache, con
 
 static size_t qk_bwd_workspace(int d) { return align256((size_t)2 * kQkBwdBlocks * d * sizeof(float)); }
 
-static size_t paged_workspace(int B, int Nq, int H, int Hk, int Nk, int d, size_t* ml_at) {
-  const int chunk = paged_chunk(B, Nq, H, Hk, Nk);
-  const size_t slots = (size_t)B * Nq * H * ((Nk + (long long)chunk - 1) / chunk);
-  *ml_at = align256(slots * d * sizeof(float));
-  return *ml_at + align256(slots * 2 * sizeof(float));
+static size_t decode_paged_workspace(int B, int Nq, int H, int Hk, int Nk, int d, size_t* ml_at) {
+  size_t o_bytes, ml_bytes;
+  paged_workspace(B, Nq, H, Hk, Nk, d, &o_bytes, &ml_bytes);
+  *ml_at = align256(o_bytes);
+  return *ml_at + align256(ml_bytes);
 }
 
 }  // namespace fa
@@ -222,7 +223,7 @@ static bool paged_sizes(int B, int Nq, int H, int Hk, int Nk, int d) {
 size_t fa_decode_paged_workspace_bytes(int B, int Nq, int H, int Hk, int Nk, int d) {
   if (!paged_sizes(B, Nq, H, Hk, Nk, d)) return 0;
   size_t ml_at;
-  return paged_workspace(B, Nq, H, Hk, Nk, d, &ml_at);
+  return decode_paged_workspace(B, Nq, H, Hk, Nk, d, &ml_at);
 }
 
 int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse, const int32_t* page_table,
@@ -238,7 +239,7 @@ int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, voi
   const long long rows = (long long)(H / Hk) * Nq;
   if (B > 65535 || rows > 0x3fffffffLL || (rows + 15) / 16 * Hk > 65535) return FA_ERR_UNSUPPORTED;  // grid y, z
   size_t ml_at;
-  const size_t need = paged_workspace(B, Nq, H, Hk, Nk, d, &ml_at);
+  const size_t need = decode_paged_workspace(B, Nq, H, Hk, Nk, d, &ml_at);
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes_ < need)
     return FA_ERR_INVALID_ARG;
   const PagedDecodeArgs a = {q, o, lse, reinterpret_cast<float*>(workspace),

@@ -418,7 +418,7 @@ int fa_rope_table(float* cos_t, float* sin_t, int table_rows, int rot_dim, doubl
  * page_table[b, j / page_size], slot j % page_size.  Entries behind a sequence's
  * last page are not read.  seqlens_k is a device int32 [B] of key counts.
  * page_size: a multiple of 16 (FA_ERR_UNSUPPORTED otherwise), max_pages·page_size
- * at most 2^30; the caches 16-byte aligned, fa_cache_bytes(...) bytes each.
+ * at most 2^30, a page (Hk·page_size rows) below 2^31 bytes in 16 bits; the caches 16-byte aligned, fa_cache_bytes(...) bytes each.
  * Rows are [num_pages, Hk, page_size]; the rows of one page and head are one block:
  *   FA_CACHE_16BIT  page_size rows of d elements of the dtype.
  *   FA_CACHE_INT4   page_size rows of d/2 bytes, then page_size rows of d/32 pairs
