@@ -1,9 +1,9 @@
 // fa_paged.cu — attention of a few new queries per sequence over a paged key/value cache, 16-bit or 4-bit.
 //
 //   fa_paged_split_kernel  one wave of blocks; the keys of all (sequence, key head, tile of query rows) units,
-//                          in granules of 64 keys, are dealt out evenly: each block takes a run of granules,
-//                          which may end inside a unit and may span several.  A unit that lies in one run is
-//                          finished there; of others each block leaves its partial (m, ℓ, Õ = Σ_j 2^(s_j − m) v_j),
+//                          in granules of four warps' tiles, are dealt out evenly: each block takes a run of
+//                          granules, which may end inside a unit and may span several.  A unit that lies in one
+//                          run is finished there; of others each block leaves its partial (m, ℓ, Õ = Σ_j 2^(s_j − m) v_j),
 //                          s = scale·log2(e)·q·k (base 2)
 //   fa_paged_merge_kernel  joins the parts of a row: m = max m_c, ℓ = Σ ℓ_c·2^(m_c − m), Õ the same way
 //
@@ -14,9 +14,9 @@
 // rows of keys in shared memory in its own layout, and the 4-bit numbers would have to be written there
 // after unpacking.
 //
-// Each warp streams its own 16-key tiles (every fourth 16 keys of the run) through a ring in shared memory
-// with asynchronous 16-byte copies; the ring's depth covers the latency of HBM, and no warp waits for another
-// until the end of a unit.
+// Each warp streams its own tiles (16 keys, or 32 of 4 bits) through a ring in shared memory with asynchronous
+// 16-byte copies; the ring's depth covers the latency of HBM, and no warp waits for another until the end of
+// a unit.
 //
 // Orders are chosen so that no operand moves between lanes.  With g = lane/4, t = lane%4:
 //   scores   Sᵀ[16 keys × 8 rows] = K·qᵀ.  A lane reads whole 16-byte pieces of keys g and g + 8 and takes the
@@ -26,41 +26,49 @@
 // A lane's scores and outputs belong to the same two rows (2t, 2t+1), so rescaling needs no exchange either.
 // The pieces are written to shared memory at places that keep these reads free of bank conflicts.
 //
-// 4-bit numbers are used where they lie: a masked half word with n in bits 0-3 is the fp16 n·2^-24, with n in
-// bits 4-7 n·2^-20 (subnormal, and exact in the products).  The queries are taken to fp16 by a power of two per
-// row that brings the largest to 2^12 (exact but for features 2^-26 below it), those that meet the 2^-20 form by
-// 2^-4 less.  Each group of 32 features has its own fp32 accumulator, so its scale and minimum enter once per key:
-//   s = Σ_w scale_w·(q·n)_w + min_w·(Σ q)_w.
-// For the output the values' numbers are taken to n − 8 (one exact fp16 subtraction), the value's scale multiplies P
-// before P is rounded to fp16, and Σ_j p_j·(min_j + 8·scale_j) is kept in fp32.  Without the shift the products would
-// add up to a mean of 2 standard deviations per key that the minimum takes away again: over 131071 keys the tensor
-// cores' truncating sums then left 8e-4 of the output (now 2e-4, fp16's own rounding).  A power of two above every
-// value scale the warp has met brings P·scale under 2^14; it follows the scales as the reference follows the scores.
+// The reference of the exponents rises only when a score passes it by 2^8 (one vote per tile).  P of 16-bit caches is
+// the sum of two 16-bit parts, so its rounding stays behind the output's.
 //
-// The reference rises only when a score passes it by 2^8 (one vote per tile); P of 16-bit caches is the sum of two
-// 16-bit parts, so its rounding stays behind the output's.
+// 4 bits.  The instruction count bounds this path, so everything is arranged to keep it low (a tile of 16 keys by 8
+// rows of d = 128 has 2,560 bytes to read and 4,096 numbers to unpack):
+//   * Numbers are used where they lie: a masked half word with n in bits 0-3 is the fp16 n·2^-24, with n in bits 4-7
+//     n·2^-20 (subnormal, and exact in the products).  The queries are taken to fp16 by a power of two per row that
+//     brings the largest to 2^12 (exact but for features 2^-26 below it), those that meet the 2^-20 form by 2^-4 less.
+//   * Each group of 32 features has its own fp32 accumulator, which the key's scale multiplies; the minima times the
+//     sums of q over the groups are one small product (the sums as two fp16 parts).
+//   * P is rounded to fp16 and transposed once; for each group it is then multiplied by the values' scales of its keys.
+//   * Σ_j p_j·min_j and Σ_j p_j·scale_j are one small product more, with P in two parts.
+//   * The values enter as n − 8.  Without the shift the products would add up to a mean of 2 standard deviations per
+//     key that the minimum takes away again: over 131071 keys the tensor cores' truncating sums left 8e-4 of the
+//     output.  For one row tile −8·ΣP is a product of its own (no instruction per number); two row tiles share a
+//     subtraction per number.
+//   * The reference is 2^7 below the maximum (less where scales pass 1), so that fp16's range serves P from 2^15 down.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace fa {
 
 constexpr int kPagedWarps = 4;
 constexpr int kPagedThreads = 32 * kPagedWarps;
-constexpr int kGranule = 16 * kPagedWarps;  // keys: one tile for each warp
 constexpr float kRise = 8.f;  // how far a score may pass the reference before the reference follows
 
-// Ring depth and blocks per SM of a variant: at least 40 KB in flight per SM (HBM latency times its bandwidth share),
-// within 227 KB of shared memory and the registers.
+// Tile, ring depth and blocks per SM of a variant: at least 40 KB in flight per SM (HBM latency times its share of the
+// bandwidth), within 227 KB of shared memory and the registers.
 template <int D, bool Q4, int NT>
 struct PagedConfig {
-  static constexpr int kTileBytes = 16 * (Q4 ? 2 * (D / 2 + D / 8) : 2 * D * 2);  // keys and values of 16 tokens
-  static constexpr int kStages = Q4 ? 5 : 3;
-  static constexpr int kBlocks = NT == 2 ? (D == 128 ? 2 : 4) : (!Q4 && D == 128 ? 2 : 4);
+  static constexpr int kTile = Q4 ? 32 : 16;             // keys of a warp's tile
+  static constexpr int kGranule = kTile * kPagedWarps;   // keys of all warps' tiles
+  static constexpr int kTileBytes = kTile * (Q4 ? 2 * (D / 2 + D / 8) : 2 * D * 2);
+  static constexpr int kStages = Q4 && (D == 64 || NT == 2) ? 4 : 3;
+  static constexpr int kBlocks = D == 64 ? (NT == 2 ? 3 : 4) : NT == 2 || !Q4 ? 2 : 3;
   static constexpr int kRing = kPagedWarps * kStages * kTileBytes;
   static constexpr int kRows = 8 * NT;
   static constexpr int kPitch = D + 4;  // floats per row of the warps' partial outputs
   static constexpr int kJoin = kPagedWarps * kRows * kPitch * 4;
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
 };
+constexpr int granule_keys(bool q4) { return q4 ? PagedConfig<64, true, 1>::kGranule : PagedConfig<64, false, 1>::kGranule; }
 
 struct PagedParams {
   const uint8_t* q;
@@ -70,7 +78,7 @@ struct PagedParams {
   float* part_ml;  // [2·workers, rows of a tile, 2]
   PagedArgs pg;
   int Nq, H, G, most, R, tiles;  // G = H/Hk, most: the largest length allowed, R = G·Nq rows of a key head in `tiles` tiles
-  int workers;
+  int workers, granule;
   float scale_log2;
 };
 
@@ -88,6 +96,12 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 __device__ __forceinline__ void mma_16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// 16 × 8 × 8 with a zero sum to start from.
+__device__ __forceinline__ void mma_1688_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3]) : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 
 // Transpose of an 8×8 matrix of 16-bit elements: lane (g, t) gives row g, columns 2t, 2t+1 and gets the same of the transpose.
@@ -111,7 +125,7 @@ __device__ __forceinline__ int paged_length(const PagedParams& p, int b) {
   return L < 0 || L > p.most ? -1 : L;
 }
 
-__device__ __forceinline__ int granules(int L) { return L <= 0 ? 0 : (L + kGranule - 1) / kGranule; }
+__device__ __forceinline__ int granules(const PagedParams& p, int L) { return L <= 0 ? 0 : (L + p.granule - 1) / p.granule; }
 
 // Granules of the sequences before sequence `end` (one key head, one row tile).  Every lane gets the sum; a
 // warp reads 128 lengths at a time (of at most 2^24 granules each).
@@ -123,7 +137,7 @@ __device__ __forceinline__ long long granules_before(const PagedParams& p, int e
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int b = b0 + 32 * i + lane;
-      if (b < end) n += granules(paged_length(p, b));
+      if (b < end) n += granules(p, paged_length(p, b));
     }
     sum += __reduce_add_sync(0xffffffffu, n);
   }
@@ -135,7 +149,7 @@ __device__ __forceinline__ int find_granule(const PagedParams& p, long long at, 
   const int lane = (int)lane_id();
   long long sum = 0;
   for (int b0 = 0; b0 < p.pg.B; b0 += 32) {
-    const int n = b0 + lane < p.pg.B ? granules(paged_length(p, b0 + lane)) : 0;
+    const int n = b0 + lane < p.pg.B ? granules(p, paged_length(p, b0 + lane)) : 0;
     int incl = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -197,6 +211,17 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.b32 %0, [%1 + %2];" : "=r"(v) : "r"(a), "n"(OFF));
   return v;
 }
+template <int OFF>
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1 + %2];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(a), "n"(OFF));
+  return v;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -217,49 +242,587 @@ __device__ __forceinline__ int v4_piece(int r, int c) {
 }
 
 // Copies tiles of a key head into one warp's ring.  All that does not change from tile to tile is kept per lane: where
-// its pieces lie in a tile (the swizzles repeat after 32 pieces) and in a block of page 0.
+// its pieces lie in a tile (the swizzles repeat after a copy of 32 pieces) and in a block of page 0.
+// A 16-bit tile is 16 rows of keys, 16 of values; a 4-bit one 32 rows of the keys' numbers, of the values' numbers, of
+// the keys' pairs, of the values' pairs.
 template <int D, bool Q4>
 struct TileCopy {
   static constexpr int kRow = Q4 ? D / 2 : D * 2;  // bytes of a row of elements or numbers
-  static constexpr int kPer = 16 * kRow / 512;     // 32-piece copies of 16 rows
-  static constexpr int kPairs = D / 8;             // 4 bits: pieces of 16 rows of pairs
-  const uint8_t *k, *v, *pair;
-  uint32_t dk, dv, dpair, page_bytes;
-  bool has_pair;
+  static constexpr int kPair = D / 8;              // bytes of a row of pairs
+  static constexpr int kT = Q4 ? 32 : 16;
+  static constexpr int kPer = 16 * kRow / 512;     // copies of 16 rows
+  const uint8_t *k, *v, *pair, *half_pair;
+  uint32_t dk, dv, dpair, dhalf, page_bytes;
+  uintptr_t to_v;  // from the keys' address to the values'
+  int lane;
 
-  __device__ __forceinline__ TileCopy(const PagedArgs& pg, int hk, uint32_t ring, int lane) {
+  __device__ __forceinline__ TileCopy(const PagedArgs& pg, int hk, uint32_t ring, int lane_) : lane(lane_) {
     const size_t block = cache_block_bytes(D, pg.page_size, Q4);
-    k = static_cast<const uint8_t*>(pg.k_cache) + hk * block + lane * 16;
-    v = static_cast<const uint8_t*>(pg.v_cache) + hk * block + lane * 16;
+    const uint8_t* kb = static_cast<const uint8_t*>(pg.k_cache) + hk * block;
+    const uint8_t* vb = static_cast<const uint8_t*>(pg.v_cache) + hk * block;
+    k = kb + lane * 16;
+    v = vb + lane * 16;
+    to_v = reinterpret_cast<uintptr_t>(vb) - reinterpret_cast<uintptr_t>(kb);
     page_bytes = (uint32_t)(block * pg.Hk);  // below 2^31 (checked on the host)
     const int r = lane / (kRow / 16), c = lane % (kRow / 16);
     if constexpr (Q4) {
       dk = ring + 16 * lane;
-      dv = ring + 16 * kRow + 16 * v4_piece<D>(r, c);
-      has_pair = lane < 2 * kPairs;
-      pair = static_cast<const uint8_t*>(lane < kPairs ? pg.k_cache : pg.v_cache) + hk * block + (size_t)pg.page_size * kRow +
-             lane % kPairs * 16;
-      dpair = ring + 32 * kRow + 16 * lane;
+      dv = ring + kT * kRow + 16 * v4_piece<D>(r, c);
+      // pairs of 32 rows: d = 128 has 32 pieces of the keys' and of the values', d = 64 16 each, side by side
+      const size_t rows = (size_t)pg.page_size * kRow;
+      pair = D == 128 ? kb + rows + lane * 16 : (lane < 16 ? kb : vb) + rows + lane % 16 * 16;
+      dpair = ring + 2 * kT * kRow + 16 * lane;
+      // of 16 rows: half as many
+      const int n = kPair, u = lane % n;
+      half_pair = (lane < n ? kb : vb) + rows + u * 16;
+      dhalf = ring + 2 * kT * kRow + (lane < n ? 0 : kT * kPair) + 16 * u;
     } else {
       dk = ring + 16 * k_piece<D>(r, c);
-      dv = ring + 16 * kRow + 16 * v_piece<D>(r, c);
+      dv = ring + kT * kRow + 16 * v_piece<D>(r, c);
     }
   }
 
-  // the 16 tokens from `slot` on of `page`, to the stage `at` bytes into the ring
-  __device__ __forceinline__ void copy(int page, int slot, uint32_t at) const {
+  // N·16 tokens from `slot` on of `page`, to rows 16·half … of the stage `at` bytes into the ring
+  template <int N>
+  __device__ __forceinline__ void rows(int page, int slot, uint32_t at, int half) const {
     const size_t off = (size_t)(uint32_t)page * page_bytes;
     const uint8_t* ks = k + off + slot * kRow;
     const uint8_t* vs = v + off + slot * kRow;
+    at += half * 16 * kRow;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < N * kPer; ++i) {
       // 16 bits: two (d = 128) or four rows per copy, so the values' swizzle changes with i
       const uint32_t turn = Q4 ? 0 : D == 128 ? i % 4 * 32 : i % 2 * 64;
       cp_async16(dk + at + 512 * i, ks + 512 * i);
       cp_async16(((dv + at) ^ turn) + 512 * i, vs + 512 * i);
     }
     if constexpr (Q4) {
-      if (has_pair) cp_async16(dpair + at, pair + off + slot * (D / 8));
+      at -= half * 16 * kRow;
+      if constexpr (N == 2) {
+        const uint8_t* src = pair + off + slot * kPair;
+        cp_async16(dpair + at, src);
+        if constexpr (D == 128) cp_async16(dpair + at + kT * kPair, reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(src) + to_v));
+      } else {
+        if (lane < 2 * kPair) cp_async16(dhalf + at + half * 16 * kPair, half_pair + off + slot * kPair);
+      }
+    }
+  }
+};
+
+// What a warp holds of its query rows, and one tile's work, for a 16-bit cache.
+template <int D, bool BF16, int NT>
+struct Rows16 {
+  static constexpr int W = D / 32, KS = D / 16, ROW = D * 2;
+  uint32_t qb[NT][KS][2];
+  float m[NT][2], mz[NT][2], rise_at[NT][2];  // the reference, with 0 for −inf, and the dot product from which it has to rise
+  float l[NT][2], o[NT][KS][4];
+  int lim[NT][2];  // the last key each of this lane's rows (2t, 2t+1) sees
+  uint32_t lane_k0, lane_k1, lane_v;
+  float coef;
+  int g, t, L, Nq;
+
+  __device__ __forceinline__ void init(const PagedParams& p, int b, int hk, int r0, int len, int lane) {
+    g = lane >> 2;
+    t = lane & 3;
+    L = len;
+    Nq = p.Nq;
+    coef = p.scale_log2;
+    // where this lane reads in a tile, but for constants: keys of row g (even and odd 64-byte pieces, which the swizzle
+    // swaps in odd rows), values of row 2t
+    lane_k0 = 16 * k_piece<D>(g, t);
+    lane_k1 = 16 * k_piece<D>(g, 4 + t);
+    lane_v = 16 * ROW + 16 * v_piece<D>(2 * t, g);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = r0 + 8 * nt + g;
+      const bool on = r < p.R;
+      const uint8_t* src = p.q + (on ? paged_row(p, b, hk, r) : 0) * D * 2;
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(src + (32 * j + 8 * t) * 2)) : make_uint4(0, 0, 0, 0);
+        qb[nt][2 * j][0] = v.x;
+        qb[nt][2 * j][1] = v.y;
+        qb[nt][2 * j + 1][0] = v.z;
+        qb[nt][2 * j + 1][1] = v.w;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int rr = r0 + 8 * nt + 2 * t + u;
+        lim[nt][u] = L - Nq + (rr < p.R ? rr / p.G : Nq - 1);
+        m[nt][u] = rise_at[nt][u] = -INFINITY;
+        mz[nt][u] = l[nt][u] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nt][j][i] = 0.f;
+    }
+  }
+
+  __device__ __forceinline__ void step(uint32_t tile, int j0, uint32_t) {
+    const bool tail = j0 + 16 > L;
+    // ---- scores of keys j0 + g and j0 + g + 8
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const uint32_t a = tile + (j & 1 ? lane_k1 : lane_k0) + j / 2 * 128;
+      const uint4 x = lds128<0>(a), y = lds128<8 * ROW>(a);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_16816<BF16>(s[nt], x.x, y.x, x.y, y.y, qb[nt][2 * j][0], qb[nt][2 * j][1]);
+        mma_16816<BF16>(s[nt], x.z, y.z, x.w, y.w, qb[nt][2 * j + 1][0], qb[nt][2 * j + 1][1]);
+      }
+    }
+    // ---- keys behind a row's last one; rows behind the sequence's end hold anything, so they are replaced, not scaled
+    if (j0 + 15 > L - Nq) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j0 + g + 8 * (i >> 1) > lim[nt][i & 1]) s[nt][i] = -INFINITY;
+    }
+    // ---- the reference (NaN does not raise it: it reaches the sums all the same)
+    bool rise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      rise = rise || fmaxf(s[nt][0], s[nt][2]) > rise_at[nt][0] || fmaxf(s[nt][1], s[nt][3]) > rise_at[nt][1];
+    if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float x = fmaxf(s[nt][u], s[nt][2 + u]);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+          const float mn = fmaxf(m[nt][u], x * coef);
+          const float alpha = m[nt][u] == -INFINITY ? 0.f : ex2(m[nt][u] - mn);
+          m[nt][u] = mn;
+          mz[nt][u] = mn == -INFINITY ? 0.f : mn;
+          rise_at[nt][u] = (mn + kRise) / coef;
+          l[nt][u] *= alpha;
+#pragma unroll
+          for (int j = 0; j < KS; ++j) {
+            o[nt][j][u] *= alpha;
+            o[nt][j][2 + u] *= alpha;
+          }
+        }
+    }
+    // ---- probabilities, in two parts, transposed
+    uint32_t bh[NT][2], bl[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float pr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pr[i] = ex2(fmaf(s[nt][i], coef, -mz[nt][i & 1]));
+      l[nt][0] += pr[0] + pr[2];
+      l[nt][1] += pr[1] + pr[3];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t hi = pack2<BF16>(pr[2 * u], pr[2 * u + 1]);
+        const float2 back = unpack2<BF16>(hi);
+        bh[nt][u] = movmatrix_trans(hi);
+        bl[nt][u] = movmatrix_trans(pack2<BF16>(pr[2 * u] - back.x, pr[2 * u + 1] - back.y));
+      }
+    }
+    // ---- output
+    const int key[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
+    const bool apart = Nq > 1 && j0 + 15 > L - Nq;
+#pragma unroll
+    for (int cc = 0; cc < D / 64; ++cc) {
+      uint32_t v[4][4];
+      const uint32_t av = tile + lane_v + 128 * cc;
+      const uint4 rows[4] = {lds128<0>(av), lds128<ROW>(av), lds128<8 * ROW>(av), lds128<9 * ROW>(av)};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i][0] = rows[i].x;
+        v[i][1] = rows[i].y;
+        v[i][2] = rows[i].z;
+        v[i][3] = rows[i].w;
+      }
+      if (tail) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (j0 + key[i] >= L) v[i][u] = 0u;
+      }
+      if (!apart) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a0 = prmt(v[0][i], v[1][i], 0x5410u), a1 = prmt(v[0][i], v[1][i], 0x7632u);
+          const uint32_t a2 = prmt(v[2][i], v[3][i], 0x5410u), a3 = prmt(v[2][i], v[3][i], 0x7632u);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16816<BF16>(o[nt][4 * cc + i], a0, a1, a2, a3, bh[nt][0], bh[nt][1]);
+            mma_16816<BF16>(o[nt][4 * cc + i], a0, a1, a2, a3, bl[nt][0], bl[nt][1]);
+          }
+        }
+      } else {
+        // the last keys, which the new tokens see one after another: a token at a time with the values behind it
+        // taken out, since an infinity or NaN there would pass a zero probability
+#pragma unroll 1
+        for (int end_key = max(j0, L - Nq); end_key < min(j0 + 16, L); ++end_key) {
+          const bool top = end_key == j0 + 15;  // rows that see all of this tile, and more
+          uint32_t x[4][4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[u][i] = j0 + key[u] <= end_key ? v[u][i] : 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = prmt(x[0][i], x[1][i], 0x5410u), a1 = prmt(x[0][i], x[1][i], 0x7632u);
+            const uint32_t a2 = prmt(x[2][i], x[3][i], 0x5410u), a3 = prmt(x[2][i], x[3][i], 0x7632u);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float tmp[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_16816<BF16>(tmp, a0, a1, a2, a3, bh[nt][0], bh[nt][1]);
+              mma_16816<BF16>(tmp, a0, a1, a2, a3, bl[nt][0], bl[nt][1]);
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (lim[nt][u & 1] == end_key || (top && lim[nt][u & 1] > end_key)) o[nt][4 * cc + i][u] += tmp[u];
+            }
+          }
+        }
+      }
+    }
+  }
+
+  // Row 8·nt + 2t + u of the warp's output (features [0, D) of `row`); its sum over this lane's keys is l[nt][u].
+  __device__ __forceinline__ void store(float* row, int nt, int u) const {
+#pragma unroll
+    for (int cc = 0; cc < D / 64; ++cc)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        row[64 * cc + 8 * g + 2 * i] = o[nt][4 * cc + i][u];
+        row[64 * cc + 8 * g + 2 * i + 1] = o[nt][4 * cc + i][2 + u];
+      }
+  }
+};
+
+// The same for a 4-bit cache; a tile is two sub-tiles of 16 keys.
+template <int D, bool BF16, int NT>
+struct Rows4 {
+  static constexpr int W = D / 32, KS = D / 16, ROW = D / 2, PAIR = D / 8;
+  static constexpr bool kCentre = NT == 1;  // −8·ΣP as a product
+  static constexpr float kDepth = 7.f;      // the reference is 2^7 under the maximum
+  uint32_t qb[NT][KS][2], qs[NT];
+  float m[NT][2], mz[NT][2], rise_at[NT][2];
+  float l[NT][2], o[NT][KS][4], mins[NT][4], coef[NT][2];
+  int lim[NT][2];
+  uint32_t lane_k, lane_v, lane_p, lane_m, lane_a, lane_s;
+  float cap, cap_value;  // a power of two (and its log2), at least 1, that no value scale of the warp passes
+  int g, t, lane, L, Nq;
+
+  __device__ __forceinline__ void init(const PagedParams& p, int b, int hk, int r0, int len, int lane_) {
+    lane = lane_;
+    g = lane >> 2;
+    t = lane & 3;
+    L = len;
+    Nq = p.Nq;
+    cap = 0.f;
+    cap_value = 1.f;
+    lane_k = lane * PAIR;  // 16 (8) bytes of row g from 16t (8t) on
+    lane_v = 32 * ROW + (D == 128 ? 16 * v4_piece<D>(2 * t, g >> 1) + 8 * (g & 1) : 16 * v4_piece<D>(2 * t, g >> 2) + 4 * (g & 3));
+    lane_p = 64 * ROW + g * PAIR;                          // the keys' pairs of row g
+    lane_m = lane_p + (W == 4 ? (t & 1) * 8 : 0);          // two of them: the minima of groups 2t, 2t + 1 (mod 4)
+    lane_s = 64 * ROW + 32 * PAIR + 2 * t * PAIR;          // the values' pairs of row 2t
+    lane_a = lane_s + (g & (W - 1)) * 4 + (g < 4 ? 2 : 0); // its minimum (g < 4) or scale of group g mod 4
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = r0 + 8 * nt + g;
+      const bool on = r < p.R;
+      const uint8_t* src = p.q + (on ? paged_row(p, b, hk, r) : 0) * D * 2;
+      float f[W][8], most = 0.f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(src + (32 * j + 8 * t) * 2)) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = unpack2<BF16>(w[i]);
+          f[j][2 * i] = x.x;
+          f[j][2 * i + 1] = x.y;
+          most = fmaxf(most, fmaxf(fabsf(x.x), fabsf(x.y)));
+        }
+      }
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      // most = x·2^e, 1 <= x < 2; the row goes into the products as q·2^(12 − e), times n·2^-24: s = s'·2^(e + 12).  The
+      // sums of 32 features go as Σq·2^(8 − e), below 2^14, in two parts
+      const int e = min(max((int)(__float_as_uint(most) >> 23) - 127, -100), 100);
+      const float up = __uint_as_float((uint32_t)(127 + 12 - e) << 23);
+      const float sums_up = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+      float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const float even = up, odd = up * 0.0625f;  // the factors beside n·2^-24 and n·2^-20
+        qb[nt][2 * j][0] = pack2<false>(f[j][0] * even, f[j][4] * even);
+        qb[nt][2 * j][1] = pack2<false>(f[j][1] * odd, f[j][5] * odd);
+        qb[nt][2 * j + 1][0] = pack2<false>(f[j][2] * even, f[j][6] * even);
+        qb[nt][2 * j + 1][1] = pack2<false>(f[j][3] * odd, f[j][7] * odd);
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += f[j][i];
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        s *= sums_up;
+        hi[j] = __half2float(__float2half_rn(s));
+        lo[j] = s - hi[j];
+      }
+      // k-index 0-3: the first parts of groups 0-3, 4-7: the second parts
+      qs[nt] = t == 0 ? pack2<false>(hi[0], hi[1]) : t == 1 ? pack2<false>(hi[2], hi[3])
+             : t == 2 ? pack2<false>(lo[0], lo[1]) : pack2<false>(lo[2], lo[3]);
+      const float back = __uint_as_float((uint32_t)(127 + 12 + e) << 23) * p.scale_log2;
+      coef[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+      coef[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int rr = r0 + 8 * nt + 2 * t + u;
+        lim[nt][u] = L - Nq + (rr < p.R ? rr / p.G : Nq - 1);
+        m[nt][u] = rise_at[nt][u] = -INFINITY;
+        mz[nt][u] = l[nt][u] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mins[nt][i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nt][j][i] = 0.f;
+    }
+  }
+
+  __device__ __forceinline__ void step(uint32_t tile, int j0, uint32_t flags) {
+    const bool special = j0 + 32 > L || flags != 3u;  // some keys are not there
+    auto live = [&](int sub, int key) { return ((flags >> sub) & 1u) != 0u && j0 + 16 * sub + key < L; };
+    // ---- the largest value scale: lane r looks at row r
+    float most;
+    {
+      uint32_t w[W];
+      const uint32_t a = tile + 64 * ROW + 32 * PAIR + lane * PAIR;
+      if constexpr (W == 4) {
+        const uint4 x = lds128<0>(a);
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+      } else {
+        const uint2 x = lds64<0>(a);
+        w[0] = x.x; w[1] = x.y;
+      }
+      __half2 top = *reinterpret_cast<const __half2*>(&w[0]);
+#pragma unroll
+      for (int j = 1; j < W; ++j) top = __hmax2(top, *reinterpret_cast<const __half2*>(&w[j]));
+      most = __low2float(top);
+      if (special && !live(lane >> 4, lane & 15)) most = 0.f;
+    }
+    // ---- scores of keys j0 + 16·sub + g and + 8
+    float s[2][NT][4];
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      uint32_t kn[2][W], kp[2][W], mn[2];
+      const uint32_t ak = tile + lane_k + sub * 16 * ROW, ap = tile + lane_p + sub * 16 * PAIR, am = tile + lane_m + sub * 16 * PAIR;
+      if constexpr (W == 4) {
+        const uint4 x0 = lds128<0>(ak), x1 = lds128<8 * ROW>(ak), y0 = lds128<0>(ap), y1 = lds128<8 * PAIR>(ap);
+        kn[0][0] = x0.x; kn[0][1] = x0.y; kn[0][2] = x0.z; kn[0][3] = x0.w;
+        kn[1][0] = x1.x; kn[1][1] = x1.y; kn[1][2] = x1.z; kn[1][3] = x1.w;
+        kp[0][0] = y0.x; kp[0][1] = y0.y; kp[0][2] = y0.z; kp[0][3] = y0.w;
+        kp[1][0] = y1.x; kp[1][1] = y1.y; kp[1][2] = y1.z; kp[1][3] = y1.w;
+        const uint2 z0 = lds64<0>(am), z1 = lds64<8 * PAIR>(am);
+        mn[0] = prmt(z0.x, z0.y, 0x7632u);
+        mn[1] = prmt(z1.x, z1.y, 0x7632u);
+      } else {
+        const uint2 x0 = lds64<0>(ak), x1 = lds64<8 * ROW>(ak), y0 = lds64<0>(ap), y1 = lds64<8 * PAIR>(ap);
+        kn[0][0] = x0.x; kn[0][1] = x0.y; kn[1][0] = x1.x; kn[1][1] = x1.y;
+        kp[0][0] = y0.x; kp[0][1] = y0.y; kp[1][0] = y1.x; kp[1][1] = y1.y;
+        mn[0] = prmt(y0.x, y0.y, 0x7632u);
+        mn[1] = prmt(y1.x, y1.y, 0x7632u);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float acc[4];
+        mma_1688_first(acc, mn[0], mn[1], qs[nt]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[sub][nt][i] = acc[i] * 9.5367431640625e-07f;  // 2^-20: from 2^(8 − e) to 2^-(e + 12)
+      }
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const uint32_t x0 = kn[0][j], x1 = kn[1][j], y0 = x0 >> 8, y1 = x1 >> 8;
+        const float p0 = __low2float(*reinterpret_cast<const __half2*>(&kp[0][j]));
+        const float p1 = __low2float(*reinterpret_cast<const __half2*>(&kp[1][j]));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float acc[4];
+          mma_16816_first(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qb[nt][2 * j][0], qb[nt][2 * j][1]);
+          mma_16816<false>(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qb[nt][2 * j + 1][0],
+                           qb[nt][2 * j + 1][1]);
+          s[sub][nt][0] = fmaf(p0, acc[0], s[sub][nt][0]);
+          s[sub][nt][1] = fmaf(p0, acc[1], s[sub][nt][1]);
+          s[sub][nt][2] = fmaf(p1, acc[2], s[sub][nt][2]);
+          s[sub][nt][3] = fmaf(p1, acc[3], s[sub][nt][3]);
+        }
+      }
+    }
+    // ---- keys behind a row's last one, or that are not there: they may hold anything, so they are replaced
+    if (special || j0 + 31 > L - Nq) {
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = g + 8 * (i >> 1);
+            if (!live(sub, key) || j0 + 16 * sub + key > lim[nt][i & 1]) s[sub][nt][i] = -INFINITY;
+          }
+    }
+    // ---- the reference (NaN does not raise it: it reaches the sums all the same)
+    bool rise = most > cap_value;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        rise = rise || fmaxf(fmaxf(s[0][nt][u], s[0][nt][2 + u]), fmaxf(s[1][nt][u], s[1][nt][2 + u])) > rise_at[nt][u];
+    if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+      const float next = fmaxf(cap, (float)((int)(__float_as_uint(most) >> 23) - 126));  // 2^next is above it
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float x = fmaxf(fmaxf(s[0][nt][u], s[0][nt][2 + u]), fmaxf(s[1][nt][u], s[1][nt][2 + u]));
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+          // m is the reference: 2^(7 − cap) under the largest score when it was set
+          const float r = fmaxf(m[nt][u] + (next - cap), fmaf(x, coef[nt][u], next - kDepth));
+          const float alpha = m[nt][u] == -INFINITY ? 0.f : ex2(m[nt][u] - r);
+          m[nt][u] = r;
+          mz[nt][u] = r == -INFINITY ? 0.f : r;
+          rise_at[nt][u] = (r + (kDepth + kRise - next)) / coef[nt][u];
+          l[nt][u] *= alpha;
+          mins[nt][u] *= alpha;
+#pragma unroll
+          for (int j = 0; j < KS; ++j) {
+            o[nt][j][u] *= alpha;
+            o[nt][j][2 + u] *= alpha;
+          }
+        }
+      cap = next;
+      cap_value = exp2f(next);
+    }
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      // ---- probabilities (up to 2^(15 − cap)), in two parts, transposed
+      uint32_t bh[NT][2], bl[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float pr[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pr[i] = ex2(fmaf(s[sub][nt][i], coef[nt][i & 1], -mz[nt][i & 1]));
+        l[nt][0] += pr[0] + pr[2];
+        l[nt][1] += pr[1] + pr[3];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t hi = pack2<false>(pr[2 * u], pr[2 * u + 1]);
+          const float2 back = unpack2<false>(hi);
+          bh[nt][u] = movmatrix_trans(hi);
+          bl[nt][u] = movmatrix_trans(pack2<false>(pr[2 * u] - back.x, pr[2 * u + 1] - back.y));
+        }
+      }
+      // ---- values of keys 2t, 2t + 1, 2t + 8, 2t + 9: numbers, pairs, and one minimum or scale of each
+      uint32_t v[4][W / 2], pair[4][W], one[4];
+      const uint32_t av = tile + lane_v + sub * 16 * ROW, odd = tile + (lane_v ^ ROW) + sub * 16 * ROW;  // row 2t + 1: the swizzle
+      const uint32_t as = tile + lane_s + sub * 16 * PAIR, aa = tile + lane_a + sub * 16 * PAIR;         // turns the row's bit too
+      one[0] = lds16<0>(aa);
+      one[1] = lds16<PAIR>(aa);
+      one[2] = lds16<8 * PAIR>(aa);
+      one[3] = lds16<9 * PAIR>(aa);
+      if constexpr (W == 4) {
+        const uint2 n[4] = {lds64<0>(av), lds64<0>(odd), lds64<8 * ROW>(av), lds64<8 * ROW>(odd)};
+        const uint4 y[4] = {lds128<0>(as), lds128<PAIR>(as), lds128<8 * PAIR>(as), lds128<9 * PAIR>(as)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i][0] = n[i].x;
+          v[i][1] = n[i].y;
+          pair[i][0] = y[i].x;
+          pair[i][1] = y[i].y;
+          pair[i][2] = y[i].z;
+          pair[i][3] = y[i].w;
+        }
+      } else {
+        const uint2 y[4] = {lds64<0>(as), lds64<PAIR>(as), lds64<8 * PAIR>(as), lds64<9 * PAIR>(as)};
+        v[0][0] = lds32<0>(av);
+        v[1][0] = lds32<0>(odd);
+        v[2][0] = lds32<8 * ROW>(av);
+        v[3][0] = lds32<8 * ROW>(odd);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          pair[i][0] = y[i].x;
+          pair[i][1] = y[i].y;
+        }
+      }
+      if (special) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!live(sub, 2 * t + (i & 1) + 8 * (i >> 1))) {
+            one[i] = 0u;
+#pragma unroll
+            for (int j = 0; j < W; ++j) pair[i][j] = 0u;
+          }
+      }
+      // ---- Σ p·min (rows 0-3 of the product) and Σ p·scale (rows 4-7) of each group
+      const uint32_t a01 = prmt(one[0], one[1], 0x5410u), a89 = prmt(one[2], one[3], 0x5410u);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_16816<false>(mins[nt], a01, 0u, a89, 0u, bh[nt][0], bh[nt][1]);
+        mma_16816<false>(mins[nt], a01, 0u, a89, 0u, bl[nt][0], bl[nt][1]);
+      }
+      // ---- Σ (P·scale)·(n − 8)
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+        const uint32_t e = prmt(v[0][j >> 1], v[1][j >> 1], sel), f = prmt(v[2][j >> 1], v[3][j >> 1], sel);
+        const uint32_t s01 = prmt(pair[0][j], pair[1][j], 0x5410u), s89 = prmt(pair[2][j], pair[3][j], 0x5410u);
+        uint32_t a[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t x = u ? e >> 8 : e, y = u ? f >> 8 : f;
+          if constexpr (kCentre) {
+            a[u][0] = x & 0x000f000fu;
+            a[u][1] = x & 0x00f000f0u;
+            a[u][2] = y & 0x000f000fu;
+            a[u][3] = y & 0x00f000f0u;
+          } else {
+            a[u][0] = less8<0>(x);
+            a[u][1] = less8<4>(x);
+            a[u][2] = less8<0>(y);
+            a[u][3] = less8<4>(y);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t b0 = mul_f16x2(bh[nt][0], s01), b1 = mul_f16x2(bh[nt][1], s89);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if constexpr (kCentre)  // −8·2^-24 for the even numbers, −8·2^-20 for the odd ones
+              mma_16816<false>(o[nt][2 * j + u], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
+            mma_16816<false>(o[nt][2 * j + u], a[u][0], a[u][1], a[u][2], a[u][3], b0, b1);
+          }
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void store(float* row, int nt, int u) const {
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const float mn = __shfl_sync(0xffffffffu, mins[nt][u], 4 * j + t), sc = __shfl_sync(0xffffffffu, mins[nt][u], 4 * (j + 4) + t);
+      const float y = fmaf(8.f, sc, mn);
+      float* dst = row + 32 * j + 4 * g;
+      dst[0] = fmaf(o[nt][2 * j][u], 16777216.f, y);
+      dst[1] = fmaf(o[nt][2 * j][2 + u], 1048576.f, y);
+      dst[2] = fmaf(o[nt][2 * j + 1][u], 16777216.f, y);
+      dst[3] = fmaf(o[nt][2 * j + 1][2 + u], 1048576.f, y);
     }
   }
 };
@@ -267,24 +830,16 @@ struct TileCopy {
 template <int D, bool BF16, bool Q4, int NT>
 __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlocks)) fa_paged_split_kernel(const PagedParams p) {
   using Cfg = PagedConfig<D, Q4, NT>;
-  constexpr int W = D / 32;           // groups of 32 features
-  constexpr int KS = D / 16;          // k-steps of the scores; feature tiles of the output
-  constexpr bool MB = BF16 && !Q4;    // operand type of the products
-  constexpr int ROWS = 8 * NT, S = Cfg::kStages;
+  using Rows = std::conditional_t<Q4, Rows4<D, BF16, NT>, Rows16<D, BF16, NT>>;
+  constexpr int W = D / 32, ROWS = 8 * NT, S = Cfg::kStages, GK = Cfg::kGranule, T = Cfg::kTile;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kPagedWarps][ROWS], s_l[kPagedWarps][ROWS];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  constexpr int ROW = TileCopy<D, Q4>::kRow;  // bytes of a row of elements or numbers
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_u32(smem) + warp * S * Cfg::kTileBytes;
-  // where this lane reads in a tile: everything else is a constant apart from these.  Keys of rows g (even and odd
-  // pieces of 64 bytes: the swizzle swaps them in odd rows), values of row 2t, pairs of row g
-  const uint32_t lane_k0 = Q4 ? lane * (D / 8) : 16 * k_piece<D>(g, t), lane_k1 = Q4 ? 0 : 16 * k_piece<D>(g, 4 + t);
-  const uint32_t lane_v = 16 * ROW + (!Q4 ? 16 * v_piece<D>(2 * t, g)
-                                          : D == 128 ? 16 * v4_piece<D>(2 * t, g >> 1) + 8 * (g & 1) : 16 * v4_piece<D>(2 * t, g >> 2) + 4 * (g & 3));
-  const uint32_t lane_p = 32 * ROW + g * (D / 8);
   float* s_o = reinterpret_cast<float*>(smem);
   const int ps = p.pg.page_size;
   const int units = p.pg.Hk * p.tiles;  // of one sequence
+  const bool paired = Q4 && ps % 32 != 0;  // a tile's two halves may lie in two pages
 
   // ---- this block's run of granules
   for (int b = blockIdx.x; b < p.pg.B; b += gridDim.x)
@@ -296,7 +851,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
   if (at >= end) return;
   long long before;
   int b = find_granule(p, at / units, before);
-  int L = paged_length(p, b), n = granules(L);
+  int L = paged_length(p, b), n = granules(p, L);
   int unit = (int)((at - before * units) / n), first = (int)((at - before * units) - (long long)unit * n);
 
 #pragma unroll 1
@@ -304,30 +859,48 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
     const int last = (int)min((long long)n, first + (end - at));  // granules first .. last − 1 of this unit
     const int hk = unit % p.pg.Hk, r0 = (unit / p.pg.Hk) * ROWS;
 
-    // ---- the warp's tiles: 16 keys from 64·i + 16·warp on; page lookups run one tile ahead of the copies
+    // ---- the warp's tiles, keys GK·i + T·warp on; page lookups run one tile ahead of the copies
     const int32_t* table = p.pg.page_table + (size_t)b * p.pg.max_pages;
-    const int tiles = last - first - (kGranule * (last - 1) + 16 * warp >= L ? 1 : 0);
+    const int tiles = last - first - (GK * (last - 1) + T * warp >= L ? 1 : 0);
     const TileCopy<D, Q4> copy(p.pg, hk, ring, lane);
-    int page_i = (kGranule * first + 16 * warp) / ps, slot = (kGranule * first + 16 * warp) - page_i * ps;
-    int page = tiles > 0 ? __ldg(table + page_i) : 0;
-    int left = tiles;          // to be copied
-    uint32_t copy_at = 0;      // the stage of the next one
-    uint32_t valid = 0;        // bit i: the i-th last of them is there
+    int next_j = GK * first + T * warp;  // the first key of the next tile to be copied
+    int page_i = next_j / ps, slot = next_j - page_i * ps;
+    int page = tiles > 0 ? __ldg(table + page_i) : 0, page2 = 0;
+    auto second = [&]() { return slot + 16 >= ps ? page_i + 1 : page_i; };  // the second half's page index
+    if (paired && tiles > 0 && next_j + 16 < L) page2 = __ldg(table + second());
+    int left = tiles;      // to be copied
+    uint32_t copy_at = 0;  // the stage of the next one
+    uint32_t valid = 0;    // two bits for each of the last tiles copied: the halves that are there
     auto issue = [&]() {
+      valid *= 4;
       if (left > 0) {
         --left;
         const bool ok = (unsigned)page < (unsigned)p.pg.num_pages;
-        valid = valid * 2 + (ok ? 1u : 0u);
-        if (ok) copy.copy(page, slot, copy_at);
-        else if (lane == 0) record_status(1);
-        slot += kGranule;
+        bool bad = !ok;
+        if (!paired) {
+          if (ok) copy.template rows<T / 16>(page, slot, copy_at, 0);
+          valid += ok ? 3u : 0u;
+        } else {
+          if (ok) copy.template rows<1>(page, slot, copy_at, 0);
+          valid += ok ? 1u : 0u;
+          if (next_j + 16 < L) {
+            const bool ok2 = (unsigned)page2 < (unsigned)p.pg.num_pages;
+            if (ok2) copy.template rows<1>(page2, slot + 16 >= ps ? slot + 16 - ps : slot + 16, copy_at, 1);
+            valid += ok2 ? 2u : 0u;
+            bad = bad || !ok2;
+          }
+        }
+        if (bad && lane == 0) record_status(1);
+        next_j += GK;
+        slot += GK;
         while (slot >= ps) {
           slot -= ps;
           ++page_i;
         }
-        if (left > 0) page = __ldg(table + page_i);
-      } else {
-        valid *= 2;
+        if (left > 0) {
+          page = __ldg(table + page_i);
+          if (paired && next_j + 16 < L) page2 = __ldg(table + second());
+        }
       }
       copy_at = copy_at == (S - 1) * Cfg::kTileBytes ? 0 : copy_at + Cfg::kTileBytes;
       cp_async_commit();
@@ -335,343 +908,19 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
 #pragma unroll
     for (int s = 0; s < S - 1; ++s) issue();
 
-    // ---- queries: operand registers, and for 4 bits the row's power of two and the sums of its groups
-    uint32_t qb[NT][KS][2];
-    float coef[NT][2], qsum[NT][2][Q4 ? W : 1];
-    int lim[NT][2];  // the last key each of this lane's rows (2t, 2t+1) sees
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = r0 + 8 * nt + g;
-      const bool on = r < p.R;
-      const uint8_t* src = p.q + (on ? paged_row(p, b, hk, r) : 0) * D * 2;
-      uint32_t w[W][4];
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(src + (32 * j + 8 * t) * 2)) : make_uint4(0, 0, 0, 0);
-        w[j][0] = v.x; w[j][1] = v.y; w[j][2] = v.z; w[j][3] = v.w;
-      }
-      if constexpr (!Q4) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          qb[nt][2 * j][0] = w[j][0];
-          qb[nt][2 * j][1] = w[j][1];
-          qb[nt][2 * j + 1][0] = w[j][2];
-          qb[nt][2 * j + 1][1] = w[j][3];
-        }
-        coef[nt][0] = coef[nt][1] = p.scale_log2;
-      } else {
-        float f[W][8], most = 0.f;
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 x = unpack2<BF16>(w[j][i]);
-            f[j][2 * i] = x.x;
-            f[j][2 * i + 1] = x.y;
-            most = fmaxf(most, fmaxf(fabsf(x.x), fabsf(x.y)));
-          }
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        // most = m·2^e, 1 <= m < 2; the row goes into the products as q·2^(12 − e), times n·2^-24: s = s'·2^(e + 12)
-        const int e = min(max((int)(__float_as_uint(most) >> 23) - 127, -100), 100);
-        const float up = __uint_as_float((uint32_t)(127 + 12 - e) << 23);
-        const float down = __uint_as_float((uint32_t)(127 - 12 - e) << 23);
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const float lo = up, hi = up * 0.0625f;  // the factors beside n·2^-24 and n·2^-20
-          qb[nt][2 * j][0] = pack2<false>(f[j][0] * lo, f[j][4] * lo);
-          qb[nt][2 * j][1] = pack2<false>(f[j][1] * hi, f[j][5] * hi);
-          qb[nt][2 * j + 1][0] = pack2<false>(f[j][2] * lo, f[j][6] * lo);
-          qb[nt][2 * j + 1][1] = pack2<false>(f[j][3] * hi, f[j][7] * hi);
-          float s = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s += f[j][i];
-          s += __shfl_xor_sync(0xffffffffu, s, 1);
-          s += __shfl_xor_sync(0xffffffffu, s, 2);
-          s *= down;
-          // from the lanes of row g to the lanes that hold rows 2t, 2t+1
-          qsum[nt][0][j] = __shfl_sync(0xffffffffu, s, 8 * t);
-          qsum[nt][1][j] = __shfl_sync(0xffffffffu, s, 8 * t + 4);
-        }
-        const float back = __uint_as_float((uint32_t)(127 + 12 + e) << 23) * p.scale_log2;
-        coef[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
-        coef[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int rr = r0 + 8 * nt + 2 * t + u;
-        lim[nt][u] = L - p.Nq + (rr < p.R ? rr / p.G : p.Nq - 1);
-      }
-    }
-
-    // m: the reference (base 2), mz: the same with 0 for −inf, rise_at: the dot product from which it has to rise
-    float m[NT][2], mz[NT][2], rise_at[NT][2], l[NT][2], o[NT][KS][4], omin[NT][2][Q4 ? W : 1];
-    float cap = 0.f, up = 1.f;  // 4 bits: a power of two no value scale of the warp passes, and 2^6 / cap
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        m[nt][u] = rise_at[nt][u] = -INFINITY;
-        mz[nt][u] = 0.f;
-        l[nt][u] = 0.f;
-#pragma unroll
-        for (int j = 0; j < (Q4 ? W : 1); ++j) omin[nt][u][j] = 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < KS; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[nt][j][i] = 0.f;
-    }
-
+    Rows rows;
+    rows.init(p, b, hk, r0, L, lane);
     uint32_t tile = ring + (S - 1) * Cfg::kTileBytes;
-    int j0 = kGranule * (first - 1) + 16 * warp;
+    int j0 = GK * (first - 1) + T * warp;
 #pragma unroll 1
     for (int it = 0; it < tiles; ++it) {
       cp_async_wait<S - 2>();
       __syncwarp();  // the tile is here for every lane, and every lane is done with the one before
-      const bool have = (valid >> (S - 2)) & 1u;
+      const uint32_t flags = (valid >> (2 * (S - 2))) & 3u;
       issue();
       tile = tile == ring + (S - 1) * Cfg::kTileBytes ? ring : tile + Cfg::kTileBytes;
-      j0 += kGranule;
-      if (!have) continue;
-      const bool tail = j0 + 16 > L;
-
-      // ---- scores of keys j0 + g and j0 + g + 8
-      float s[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
-      uint32_t vp[Q4 ? 2 : 1][Q4 ? W : 1];  // (scale, min) of the values of keys g, g + 8
-      float most = 0.f;                     // the largest of these scales
-      if constexpr (!Q4) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const uint32_t a = tile + (j & 1 ? lane_k1 : lane_k0) + j / 2 * 128;
-          const uint4 x = lds128<0>(a), y = lds128<8 * ROW>(a);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_16816<MB>(s[nt], x.x, y.x, x.y, y.y, qb[nt][2 * j][0], qb[nt][2 * j][1]);
-            mma_16816<MB>(s[nt], x.z, y.z, x.w, y.w, qb[nt][2 * j + 1][0], qb[nt][2 * j + 1][1]);
-          }
-        }
-      } else {
-        uint32_t kn[2][W], kp[2][W];
-        const uint32_t ak = tile + lane_k0, ap = tile + lane_p;
-        if constexpr (W == 4) {
-          const uint4 x0 = lds128<0>(ak), x1 = lds128<8 * ROW>(ak), y0 = lds128<0>(ap), y1 = lds128<8 * 16>(ap);
-          const uint4 z0 = lds128<16 * 16>(ap), z1 = lds128<24 * 16>(ap);
-          kn[0][0] = x0.x; kn[0][1] = x0.y; kn[0][2] = x0.z; kn[0][3] = x0.w;
-          kn[1][0] = x1.x; kn[1][1] = x1.y; kn[1][2] = x1.z; kn[1][3] = x1.w;
-          kp[0][0] = y0.x; kp[0][1] = y0.y; kp[0][2] = y0.z; kp[0][3] = y0.w;
-          kp[1][0] = y1.x; kp[1][1] = y1.y; kp[1][2] = y1.z; kp[1][3] = y1.w;
-          vp[0][0] = z0.x; vp[0][1] = z0.y; vp[0][2] = z0.z; vp[0][3] = z0.w;
-          vp[1][0] = z1.x; vp[1][1] = z1.y; vp[1][2] = z1.z; vp[1][3] = z1.w;
-        } else {
-          const uint2 x0 = lds64<0>(ak), x1 = lds64<8 * ROW>(ak), y0 = lds64<0>(ap), y1 = lds64<8 * 8>(ap);
-          const uint2 z0 = lds64<16 * 8>(ap), z1 = lds64<24 * 8>(ap);
-          kn[0][0] = x0.x; kn[0][1] = x0.y; kn[1][0] = x1.x; kn[1][1] = x1.y;
-          kp[0][0] = y0.x; kp[0][1] = y0.y; kp[1][0] = y1.x; kp[1][1] = y1.y;
-          vp[0][0] = z0.x; vp[0][1] = z0.y; vp[1][0] = z1.x; vp[1][1] = z1.y;
-        }
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const uint32_t x0 = kn[0][j], x1 = kn[1][j], y0 = x0 >> 8, y1 = x1 >> 8;
-          const float2 p0 = __half22float2(*reinterpret_cast<const __half2*>(&kp[0][j]));
-          const float2 p1 = __half22float2(*reinterpret_cast<const __half2*>(&kp[1][j]));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float acc[4];
-            mma_16816_first(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qb[nt][2 * j][0],
-                             qb[nt][2 * j][1]);
-            mma_16816<false>(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qb[nt][2 * j + 1][0],
-                             qb[nt][2 * j + 1][1]);
-            s[nt][0] = fmaf(p0.x, acc[0], fmaf(p0.y, qsum[nt][0][j], s[nt][0]));
-            s[nt][1] = fmaf(p0.x, acc[1], fmaf(p0.y, qsum[nt][1][j], s[nt][1]));
-            s[nt][2] = fmaf(p1.x, acc[2], fmaf(p1.y, qsum[nt][0][j], s[nt][2]));
-            s[nt][3] = fmaf(p1.x, acc[3], fmaf(p1.y, qsum[nt][1][j], s[nt][3]));
-          }
-        }
-        if (tail) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int j = 0; j < W; ++j)
-              if (j0 + g + 8 * u >= L) vp[u][j] = 0u;
-        }
-        __half2 top = *reinterpret_cast<const __half2*>(&vp[0][0]);
-#pragma unroll
-        for (int j = 1; j < 2 * W; ++j) top = __hmax2(top, *reinterpret_cast<const __half2*>(&vp[j / W][j % W]));
-        most = __low2float(top);
-      }
-      // ---- keys behind a row's last one; rows behind the sequence's end hold anything, so they are replaced, not scaled
-      if (j0 + 15 > L - p.Nq) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (j0 + g > lim[nt][0]) s[nt][0] = -INFINITY;
-          if (j0 + g > lim[nt][1]) s[nt][1] = -INFINITY;
-          if (j0 + g + 8 > lim[nt][0]) s[nt][2] = -INFINITY;
-          if (j0 + g + 8 > lim[nt][1]) s[nt][3] = -INFINITY;
-        }
-      }
-      // ---- the reference (NaN does not raise it: it reaches the sums all the same)
-      bool rise = Q4 && most > cap;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        rise = rise || fmaxf(s[nt][0], s[nt][2]) > rise_at[nt][0] || fmaxf(s[nt][1], s[nt][3]) > rise_at[nt][1];
-      if (__any_sync(0xffffffffu, rise)) {
-        float grow = 1.f;
-        if constexpr (Q4) {
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-          if (most > cap) {
-            const uint32_t e = min((__float_as_uint(most) >> 23) + 1u, 160u);  // 2^(e − 127) is above it
-            const float next = __uint_as_float(e << 23);
-            grow = cap * __uint_as_float((254u - e) << 23);
-            cap = next;
-            up = 64.f * __uint_as_float((254u - e) << 23);
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            float x = fmaxf(s[nt][u], s[nt][2 + u]);
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float mn = fmaxf(m[nt][u], x * coef[nt][u]);
-            const float alpha = m[nt][u] == -INFINITY ? 0.f : ex2(m[nt][u] - mn);
-            m[nt][u] = mn;
-            mz[nt][u] = mn == -INFINITY ? 0.f : mn;
-            rise_at[nt][u] = (mn + kRise) / coef[nt][u];
-            l[nt][u] *= alpha;
-            const float ao = Q4 ? alpha * grow : alpha;
-#pragma unroll
-            for (int j = 0; j < KS; ++j) {
-              o[nt][j][u] *= ao;
-              o[nt][j][2 + u] *= ao;
-            }
-            if constexpr (Q4) {
-#pragma unroll
-              for (int j = 0; j < W; ++j) omin[nt][u][j] *= alpha;
-            }
-          }
-      }
-      // ---- probabilities, relative to the reference
-      float pr[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pr[nt][i] = ex2(fmaf(s[nt][i], coef[nt][i & 1], -mz[nt][i & 1]));
-        l[nt][0] += pr[nt][0] + pr[nt][2];
-        l[nt][1] += pr[nt][1] + pr[nt][3];
-      }
-      // ---- output
-      const int key[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
-      if constexpr (!Q4) {
-        uint32_t bh[NT][2], bl[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t hi = pack2<MB>(pr[nt][2 * u], pr[nt][2 * u + 1]);
-            const float2 back = unpack2<MB>(hi);
-            bh[nt][u] = movmatrix_trans(hi);
-            bl[nt][u] = movmatrix_trans(pack2<MB>(pr[nt][2 * u] - back.x, pr[nt][2 * u + 1] - back.y));
-          }
-        const bool apart = p.Nq > 1 && j0 + 15 > L - p.Nq;
-#pragma unroll
-        for (int cc = 0; cc < D / 64; ++cc) {
-          uint32_t v[4][4];
-          const uint32_t av = tile + lane_v + 128 * cc;
-          const uint4 rows[4] = {lds128<0>(av), lds128<ROW>(av), lds128<8 * ROW>(av), lds128<9 * ROW>(av)};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i][0] = rows[i].x; v[i][1] = rows[i].y; v[i][2] = rows[i].z; v[i][3] = rows[i].w;
-          }
-          if (tail) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                if (j0 + key[i] >= L) v[i][u] = 0u;
-          }
-          if (!apart) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t a0 = prmt(v[0][i], v[1][i], 0x5410u), a1 = prmt(v[0][i], v[1][i], 0x7632u);
-              const uint32_t a2 = prmt(v[2][i], v[3][i], 0x5410u), a3 = prmt(v[2][i], v[3][i], 0x7632u);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                mma_16816<MB>(o[nt][4 * cc + i], a0, a1, a2, a3, bh[nt][0], bh[nt][1]);
-                mma_16816<MB>(o[nt][4 * cc + i], a0, a1, a2, a3, bl[nt][0], bl[nt][1]);
-              }
-            }
-          } else {
-            // the last keys, which the new tokens see one after another: a token at a time with the values behind
-            // it taken out, since an infinity or NaN there would pass a zero probability
-#pragma unroll 1
-            for (int end_key = max(j0, L - p.Nq); end_key < min(j0 + 16, L); ++end_key) {
-              const bool top = end_key == j0 + 15;  // rows that see all of this tile, and more
-              uint32_t x[4][4];
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[u][i] = j0 + key[u] <= end_key ? v[u][i] : 0u;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t a0 = prmt(x[0][i], x[1][i], 0x5410u), a1 = prmt(x[0][i], x[1][i], 0x7632u);
-                const uint32_t a2 = prmt(x[2][i], x[3][i], 0x5410u), a3 = prmt(x[2][i], x[3][i], 0x7632u);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  float tmp[4] = {0.f, 0.f, 0.f, 0.f};
-                  mma_16816<MB>(tmp, a0, a1, a2, a3, bh[nt][0], bh[nt][1]);
-                  mma_16816<MB>(tmp, a0, a1, a2, a3, bl[nt][0], bl[nt][1]);
-#pragma unroll
-                  for (int u = 0; u < 4; ++u)
-                    if (lim[nt][u & 1] == end_key || (top && lim[nt][u & 1] > end_key)) o[nt][4 * cc + i][u] += tmp[u];
-                }
-              }
-            }
-          }
-        }
-      } else {
-        uint32_t v[4][W / 2];
-        const uint32_t av = tile + lane_v, odd = tile + (lane_v ^ ROW);  // row 2t + 1: the swizzle turns the row's bit too
-        if constexpr (W == 4) {
-          const uint2 rows[4] = {lds64<0>(av), lds64<0>(odd), lds64<8 * ROW>(av), lds64<8 * ROW>(odd)};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i][0] = rows[i].x;
-            v[i][1] = rows[i].y;
-          }
-        } else {
-          v[0][0] = lds32<0>(av);
-          v[1][0] = lds32<0>(odd);
-          v[2][0] = lds32<8 * ROW>(av);
-          v[3][0] = lds32<8 * ROW>(odd);
-        }
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-          const uint32_t e = prmt(v[0][j >> 1], v[1][j >> 1], sel), f = prmt(v[2][j >> 1], v[3][j >> 1], sel);
-          const uint32_t a0 = less8<0>(e), a1 = less8<4>(e), a2 = less8<0>(f), a3 = less8<4>(f);
-          const uint32_t d0 = less8<0>(e >> 8), d1 = less8<4>(e >> 8), d2 = less8<0>(f >> 8), d3 = less8<4>(f >> 8);
-          const float2 p0 = __half22float2(*reinterpret_cast<const __half2*>(&vp[0][j]));
-          const float2 p1 = __half22float2(*reinterpret_cast<const __half2*>(&vp[1][j]));
-          const float s0 = p0.x * up, s1 = p1.x * up, n0 = fmaf(8.f, p0.x, p0.y), n1 = fmaf(8.f, p1.x, p1.y);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t b0 = movmatrix_trans(pack2<false>(pr[nt][0] * s0, pr[nt][1] * s0));
-            const uint32_t b1 = movmatrix_trans(pack2<false>(pr[nt][2] * s1, pr[nt][3] * s1));
-            mma_16816<false>(o[nt][2 * j], a0, a1, a2, a3, b0, b1);
-            mma_16816<false>(o[nt][2 * j + 1], d0, d1, d2, d3, b0, b1);
-            omin[nt][0][j] = fmaf(pr[nt][0], n0, fmaf(pr[nt][2], n1, omin[nt][0][j]));
-            omin[nt][1][j] = fmaf(pr[nt][1], n0, fmaf(pr[nt][3], n1, omin[nt][1][j]));
-          }
-        }
-      }
+      j0 += GK;
+      if (flags != 0u) rows.step(tile, j0, flags);
     }
     cp_async_wait<0>();
     __syncthreads();  // every warp is done with its ring: the memory now holds the warps' partial outputs
@@ -679,37 +928,15 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int r = 8 * nt + 2 * t + u;
-        float* row = s_o + (warp * ROWS + r) * Cfg::kPitch;
-        float x = l[nt][u];
+        const int r = 8 * nt + 2 * (lane & 3) + u;
+        float x = rows.l[nt][u];
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-        if (g == 0) {
-          s_m[warp][r] = m[nt][u];
+        if (lane < 4) {
+          s_m[warp][r] = rows.m[nt][u];
           s_l[warp][r] = x;
         }
-        if constexpr (!Q4) {
-#pragma unroll
-          for (int cc = 0; cc < D / 64; ++cc)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              row[64 * cc + 8 * g + 2 * i] = o[nt][4 * cc + i][u];
-              row[64 * cc + 8 * g + 2 * i + 1] = o[nt][4 * cc + i][2 + u];
-            }
-        } else {
-#pragma unroll
-          for (int j = 0; j < W; ++j) {
-            float y = omin[nt][u][j];
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-            float* dst = row + 32 * j + 4 * g;
-            const float even = cap * 262144.f, odd = cap * 16384.f;  // 2^24 and 2^20, over the 2^6 / cap of the products
-            dst[0] = fmaf(o[nt][2 * j][u], even, y);
-            dst[1] = fmaf(o[nt][2 * j][2 + u], odd, y);
-            dst[2] = fmaf(o[nt][2 * j + 1][u], even, y);
-            dst[3] = fmaf(o[nt][2 * j + 1][2 + u], odd, y);
-          }
-        }
+        rows.store(s_o + (warp * ROWS + r) * Cfg::kPitch, nt, u);
       }
     __syncthreads();
     // ---- the block's: a warp per row, d/32 features per lane
@@ -757,7 +984,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
         ++b;
         L = paged_length(p, b);
       } while (L <= 0);
-      n = granules(L);
+      n = granules(p, L);
     }
   }
 }
@@ -771,7 +998,7 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = (int)(row % p.H), i = (int)(row / p.H % p.Nq), b = (int)(row / p.H / p.Nq);
   const int r = i * p.G + head % p.G, units = p.pg.Hk * p.tiles;
-  const int L = paged_length(p, b), n = granules(L);
+  const int L = paged_length(p, b), n = granules(p, L);
   const long long total = granules_before(p, p.pg.B) * units, share = granule_share(p, total);
   const long long from = granules_before(p, b) * units + (long long)(r / tile_rows * p.pg.Hk + head / p.G) * n;
   const int w0 = (int)(from / share), w1 = n > 0 ? (int)((from + n - 1) / share) : w0 - 1;  // the blocks that hold a part
@@ -811,14 +1038,14 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p
 static int paged_tile_rows(int R) { return R <= 8 ? 8 : 16; }
 
 // Blocks that can take a run: all that fit the GPU at once (at most four per SM), or one per granule of the longest batch.
-static int paged_workers(int B, int Hk, int tiles, int Nk, int per_sm) {
-  const long long most = (long long)B * Hk * tiles * ((Nk + kGranule - 1) / kGranule);
+static int paged_workers(int B, int Hk, int tiles, int Nk, int granule, int per_sm) {
+  const long long most = (long long)B * Hk * tiles * ((Nk + granule - 1) / granule);
   return (int)std::min<long long>(most, (long long)kSmCount * per_sm);
 }
 
 void paged_workspace(int B, int Nq, int H, int Hk, int Nk, int d, size_t* o_bytes, size_t* ml_bytes) {
   const int R = H / Hk * Nq, rows = paged_tile_rows(R), tiles = (R + rows - 1) / rows;
-  const size_t slots = (size_t)2 * paged_workers(B, Hk, tiles, Nk, 4) * rows;
+  const size_t slots = (size_t)2 * paged_workers(B, Hk, tiles, Nk, granule_keys(false), 4) * rows;
   *o_bytes = slots * d * sizeof(float);
   *ml_bytes = slots * 2 * sizeof(float);
 }
@@ -829,7 +1056,8 @@ static cudaError_t launch_paged_v(PagedParams p, int B, int Nk, cudaStream_t str
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = set_smem_once(done, reinterpret_cast<const void*>(fa_paged_split_kernel<D, BF16, Q4, NT>), Cfg::kSmem);
   if (e != cudaSuccess) return e;
-  p.workers = paged_workers(B, p.pg.Hk, p.tiles, Nk, Cfg::kBlocks);
+  p.granule = Cfg::kGranule;
+  p.workers = paged_workers(B, p.pg.Hk, p.tiles, Nk, Cfg::kGranule, Cfg::kBlocks);
   fa_paged_split_kernel<D, BF16, Q4, NT><<<p.workers, kPagedThreads, Cfg::kSmem, stream>>>(p);
   e = cudaPeekAtLastError();
   if (e != cudaSuccess) return e;
@@ -867,7 +1095,7 @@ cudaError_t launch_decode_paged(const PagedDecodeArgs& a, const PagedArgs& pg, c
   p.most = std::min(a.Nk, pg.max_pages * pg.page_size);
   p.R = p.G * a.Nq;
   p.tiles = (p.R + paged_tile_rows(p.R) - 1) / paged_tile_rows(p.R);
-  p.workers = 0;
+  p.workers = p.granule = 0;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   if (pg.d == 128) return pg.bf16 ? launch_paged_t<128, true>(p, pg.B, a.Nk, stream) : launch_paged_t<128, false>(p, pg.B, a.Nk, stream);
   return pg.bf16 ? launch_paged_t<64, true>(p, pg.B, a.Nk, stream) : launch_paged_t<64, false>(p, pg.B, a.Nk, stream);
