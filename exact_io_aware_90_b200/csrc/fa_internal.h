@@ -179,12 +179,14 @@ struct PagedDecodeArgs {
   const void* q;
   void* o;
   float* lse;
-  float* part_o;   // fp32, sizes from paged_workspace
+  float* part_o;   // sizes from paged_workspace
   float* part_ml;
+  void* units;
   int Nq, H, Nk;
   float scale;
 };
-void paged_workspace(int B, int Nq, int H, int Hk, int Nk, int d, size_t* o_bytes, size_t* ml_bytes);
+void paged_workspace(int B, int Nq, int H, int Hk, int Nk, int d, size_t* o_bytes, size_t* ml_bytes,
+                     size_t* unit_bytes);
 cudaError_t launch_cache_append(const AppendArgs& a, const RopeArgs& ra, const PagedArgs& pg, cudaStream_t stream);
 cudaError_t launch_cache_gather(const GatherArgs& a, const PagedArgs& pg, cudaStream_t stream);
 cudaError_t launch_decode_paged(const PagedDecodeArgs& a, const PagedArgs& pg, cudaStream_t stream);

@@ -37,7 +37,8 @@
 //   * Each group of 32 features has its own fp32 accumulator, which the key's scale multiplies; the minima times the
 //     sums of q over the groups are one small product (the sums as two fp16 parts).
 //   * P is rounded to fp16 and transposed once; for each group it is then multiplied by the values' scales of its keys.
-//   * Σ_j p_j·min_j and Σ_j p_j·scale_j are one small product more, with P in two parts.
+//   * Σ_j p_j·min_j and Σ_j p_j·scale_j are one small product more.  It takes the same rounded P, so what rounding
+//     leaves is relative to the value, n·scale + min, and not to the larger min.
 //   * The values enter as n − 8.  Without the shift the products would add up to a mean of 2 standard deviations per
 //     key that the minimum takes away again: over 131071 keys the tensor cores' truncating sums left 8e-4 of the
 //     output.  For one row tile −8·ΣP is a product of its own (no instruction per number); two row tiles share a
@@ -60,7 +61,7 @@ struct PagedConfig {
   static constexpr int kTile = Q4 ? 32 : 16;             // keys of a warp's tile
   static constexpr int kGranule = kTile * kPagedWarps;   // keys of all warps' tiles
   static constexpr int kTileBytes = kTile * (Q4 ? 2 * (D / 2 + D / 8) : 2 * D * 2);
-  static constexpr int kStages = Q4 && (D == 64 || NT == 2) ? 4 : 3;
+  static constexpr int kStages = Q4 ? 2 : 3;
   static constexpr int kBlocks = D == 64 ? (NT == 2 ? 3 : 4) : NT == 2 || !Q4 ? 2 : 3;
   static constexpr int kRing = kPagedWarps * kStages * kTileBytes;
   static constexpr int kRows = 8 * NT;
@@ -79,6 +80,7 @@ struct PagedParams {
   PagedArgs pg;
   int Nq, H, G, most, R, tiles;  // G = H/Hk, most: the largest length allowed, R = G·Nq rows of a key head in `tiles` tiles
   int workers, granule;
+  int4* units;  // [workers]: for the block that holds the first part of a unit: sequence, key head, first row, parts (else 0)
   float scale_log2;
 };
 
@@ -127,50 +129,50 @@ __device__ __forceinline__ int paged_length(const PagedParams& p, int b) {
 
 __device__ __forceinline__ int granules(const PagedParams& p, int L) { return L <= 0 ? 0 : (L + p.granule - 1) / p.granule; }
 
-// Granules of the sequences before sequence `end` (one key head, one row tile).  Every lane gets the sum; a
-// warp reads 128 lengths at a time (of at most 2^24 granules each).
-__device__ __forceinline__ long long granules_before(const PagedParams& p, int end) {
-  const int lane = (int)lane_id();
-  long long sum = 0;
-  for (int b0 = 0; b0 < end; b0 += 128) {
-    unsigned n = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int b = b0 + 32 * i + lane;
-      if (b < end) n += granules(p, paged_length(p, b));
-    }
-    sum += __reduce_add_sync(0xffffffffu, n);
-  }
-  return sum;
+// 64-bit quotient; most are of 32-bit numbers, which are several times faster to divide.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (long long)((unsigned)a / (unsigned)b);
+  return a / b;
 }
 
-// The sequence that holds granule `at` of the sequences' sum, and the granules before it.
-__device__ __forceinline__ int find_granule(const PagedParams& p, long long at, long long& before) {
-  const int lane = (int)lane_id();
-  long long sum = 0;
-  for (int b0 = 0; b0 < p.pg.B; b0 += 32) {
-    const int n = b0 + lane < p.pg.B ? granules(p, paged_length(p, b0 + lane)) : 0;
-    int incl = n;
+// Sum over the block of the granules of all sequences (one key head, one row tile), and this thread's part of it: the
+// sequences from `begin` on, `before` granules in front of them.
+struct GranuleScan {
+  long long total, before, mine;
+  int begin, count;
+};
+__device__ __forceinline__ GranuleScan scan_granules(const PagedParams& p) {
+  __shared__ long long s_sum[kPagedWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  GranuleScan s;
+  const int per = (p.pg.B + kPagedThreads - 1) / kPagedThreads;
+  s.begin = min((int)threadIdx.x * per, p.pg.B);
+  s.count = min(per, p.pg.B - s.begin);
+  s.mine = 0;
+#pragma unroll 4
+  for (int i = 0; i < s.count; ++i) s.mine += granules(p, paged_length(p, s.begin + i));
+  long long incl = s.mine;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += x;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, sum + incl > at);
-    if (past != 0u) {
-      const int l = __ffs(past) - 1;
-      before = sum + __shfl_sync(0xffffffffu, incl - n, l);
-      return b0 + l;
-    }
-    sum += __shfl_sync(0xffffffffu, incl, 31);
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += x;
   }
-  before = sum;
-  return p.pg.B;
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  long long base = 0;
+  s.total = 0;
+#pragma unroll
+  for (int w = 0; w < kPagedWarps; ++w) {
+    if (w < warp) base += s_sum[w];
+    s.total += s_sum[w];
+  }
+  s.before = base + incl - s.mine;
+  return s;
 }
 
 // Granules that each worker takes.
 __device__ __forceinline__ long long granule_share(const PagedParams& p, long long total) {
-  return max(1LL, (total + p.workers - 1) / p.workers);
+  return max(1LL, quotient(total + p.workers - 1, p.workers));
 }
 
 // What a part with maximum m weighs beside the maximum of all, M.  Parts without a key (m = -inf) hold zeros, or
@@ -598,6 +600,15 @@ struct Rows4 {
   __device__ __forceinline__ void step(uint32_t tile, int j0, uint32_t flags) {
     const bool special = j0 + 32 > L || flags != 3u;  // some keys are not there
     auto live = [&](int sub, int key) { return ((flags >> sub) & 1u) != 0u && j0 + 16 * sub + key < L; };
+    // ---- values that are not there get minimum and scale 0 (what the tile holds of them may be anything)
+    if (special) {
+      if (!live(lane >> 4, lane & 15)) {
+        const uint32_t a = tile + 64 * ROW + 32 * PAIR + lane * PAIR;
+#pragma unroll
+        for (int j = 0; j < W; ++j) st_shared_f32(a + 4 * j, 0u);
+      }
+      __syncwarp();
+    }
     // ---- the largest value scale: lane r looks at row r
     float most;
     {
@@ -614,7 +625,6 @@ struct Rows4 {
 #pragma unroll
       for (int j = 1; j < W; ++j) top = __hmax2(top, *reinterpret_cast<const __half2*>(&w[j]));
       most = __low2float(top);
-      if (special && !live(lane >> 4, lane & 15)) most = 0.f;
     }
     // ---- scores of keys j0 + 16·sub + g and + 8
     float s[2][NT][4];
@@ -712,8 +722,8 @@ struct Rows4 {
     }
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
-      // ---- probabilities (up to 2^(15 − cap)), in two parts, transposed
-      uint32_t bh[NT][2], bl[NT][2];
+      // ---- probabilities (up to 2^(15 − cap)), rounded to fp16 and transposed
+      uint32_t bh[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float pr[4];
@@ -722,12 +732,7 @@ struct Rows4 {
         l[nt][0] += pr[0] + pr[2];
         l[nt][1] += pr[1] + pr[3];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t hi = pack2<false>(pr[2 * u], pr[2 * u + 1]);
-          const float2 back = unpack2<false>(hi);
-          bh[nt][u] = movmatrix_trans(hi);
-          bl[nt][u] = movmatrix_trans(pack2<false>(pr[2 * u] - back.x, pr[2 * u + 1] - back.y));
-        }
+        for (int u = 0; u < 2; ++u) bh[nt][u] = movmatrix_trans(pack2<false>(pr[2 * u], pr[2 * u + 1]));
       }
       // ---- values of keys 2t, 2t + 1, 2t + 8, 2t + 9: numbers, pairs, and one minimum or scale of each
       uint32_t v[4][W / 2], pair[4][W], one[4];
@@ -761,22 +766,10 @@ struct Rows4 {
           pair[i][1] = y[i].y;
         }
       }
-      if (special) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!live(sub, 2 * t + (i & 1) + 8 * (i >> 1))) {
-            one[i] = 0u;
-#pragma unroll
-            for (int j = 0; j < W; ++j) pair[i][j] = 0u;
-          }
-      }
       // ---- Σ p·min (rows 0-3 of the product) and Σ p·scale (rows 4-7) of each group
       const uint32_t a01 = prmt(one[0], one[1], 0x5410u), a89 = prmt(one[2], one[3], 0x5410u);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        mma_16816<false>(mins[nt], a01, 0u, a89, 0u, bh[nt][0], bh[nt][1]);
-        mma_16816<false>(mins[nt], a01, 0u, a89, 0u, bl[nt][0], bl[nt][1]);
-      }
+      for (int nt = 0; nt < NT; ++nt) mma_16816<false>(mins[nt], a01, 0u, a89, 0u, bh[nt][0], bh[nt][1]);
       // ---- Σ (P·scale)·(n − 8)
 #pragma unroll
       for (int j = 0; j < W; ++j) {
@@ -841,18 +834,44 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
   const int units = p.pg.Hk * p.tiles;  // of one sequence
   const bool paired = Q4 && ps % 32 != 0;  // a tile's two halves may lie in two pages
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int step_pages = GK / ps, step_slots = GK - step_pages * ps;
+
   // ---- this block's run of granules
-  for (int b = blockIdx.x; b < p.pg.B; b += gridDim.x)
-    if (threadIdx.x == 0 && paged_length(p, b) < 0) record_status(1);
-  const long long total = granules_before(p, p.pg.B) * units;
-  const long long share = granule_share(p, total);
+  const GranuleScan scan = scan_granules(p);
+  const long long total = scan.total * units, share = granule_share(p, total);
   long long at = blockIdx.x * share;
   const long long end = min(at + share, total);
+  __shared__ int s_b;
+  __shared__ long long s_before;
+  const long long goal = quotient(at, units);
+  if (goal >= scan.before && goal < scan.before + scan.mine) {
+    long long before = scan.before;
+    int b = scan.begin;
+    for (;; ++b) {
+      const int n = granules(p, paged_length(p, b));
+      if (goal < before + n) break;
+      before += n;
+    }
+    s_b = b;
+    s_before = before;
+  }
+  // sequences without keys, and lengths that are out of range: the blocks share them out
+  for (int b = blockIdx.x; b < p.pg.B; b += gridDim.x) {
+    const int len = paged_length(p, b);
+    if (len < 0 && threadIdx.x == 0) record_status(1);
+    if (len == 0) {
+      const size_t rows = (size_t)p.Nq * p.H;
+      for (size_t i = threadIdx.x; i < rows * D; i += kPagedThreads) store_out<D, BF16>(p.o, b * rows * D + i, 0.f);
+      for (size_t i = threadIdx.x; i < rows; i += kPagedThreads) p.lse[b * rows + i] = -INFINITY;
+    }
+  }
+  if (threadIdx.x == 0) p.units[blockIdx.x] = make_int4(0, 0, 0, 0);
+  __syncthreads();
   if (at >= end) return;
-  long long before;
-  int b = find_granule(p, at / units, before);
-  int L = paged_length(p, b), n = granules(p, L);
-  int unit = (int)((at - before * units) / n), first = (int)((at - before * units) - (long long)unit * n);
+  int b = s_b, L = paged_length(p, b), n = granules(p, L);
+  const long long in_b = at - s_before * units;
+  int unit = (int)quotient(in_b, n), first = (int)(in_b - (long long)unit * n);
 
 #pragma unroll 1
   for (;;) {
@@ -892,8 +911,9 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
         }
         if (bad && lane == 0) record_status(1);
         next_j += GK;
-        slot += GK;
-        while (slot >= ps) {
+        page_i += step_pages;
+        slot += step_slots;
+        if (slot >= ps) {
           slot -= ps;
           ++page_i;
         }
@@ -942,6 +962,8 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
     // ---- the block's: a warp per row, d/32 features per lane
     const bool whole = first == 0 && last == n;
     const int part = 2 * blockIdx.x + (first == 0 ? 1 : 0);
+    if (first == 0 && last < n && threadIdx.x == 0)  // the blocks behind this one hold the rest
+      p.units[blockIdx.x] = make_int4(b, hk, r0, 1 + (int)quotient(n - last + share - 1, share));
 #pragma unroll 1
     for (int r = warp; r < ROWS && r0 + r < p.R; r += kPagedWarps) {
       float M = -INFINITY;
@@ -989,39 +1011,33 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
   }
 }
 
-// One block per row of q.  A unit that lay in one run is already written; its row has nothing to join.
+// Block (worker, row of a tile): joins that row of the unit whose first part the worker holds.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p, int tile_rows) {
+__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p) {
   constexpr int F = D / 32;
   __shared__ float s_o[4][D], s_l[4];
-  const size_t row = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int head = (int)(row % p.H), i = (int)(row / p.H % p.Nq), b = (int)(row / p.H / p.Nq);
-  const int r = i * p.G + head % p.G, units = p.pg.Hk * p.tiles;
-  const int L = paged_length(p, b), n = granules(p, L);
-  const long long total = granules_before(p, p.pg.B) * units, share = granule_share(p, total);
-  const long long from = granules_before(p, b) * units + (long long)(r / tile_rows * p.pg.Hk + head / p.G) * n;
-  const int w0 = (int)(from / share), w1 = n > 0 ? (int)((from + n - 1) / share) : w0 - 1;  // the blocks that hold a part
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // every block waits, so that this kernel ends after the other
-  if (w0 == w1 || L < 0) return;
-  // the first block's part is its last one (slot 1), the others' their first (slot 0)
-  const int at = r % tile_rows;
-  auto slot = [&](int w) { return (size_t)(2 * w + (w == w0 ? 1 : 0)) * tile_rows + at; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y, tile_rows = gridDim.y, w0 = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 unit = __ldcg(p.units + w0);  // sequence, key head, first row, parts
+  const int parts = unit.w;
+  if (parts == 0 || unit.z + r >= p.R) return;
+  // the first worker's part is its last one (slot 1), the others' their first (slot 0)
+  auto slot = [&](int i) { return (size_t)(2 * (w0 + i) + (i == 0 ? 1 : 0)) * tile_rows + r; };
   float M = -INFINITY;
-  for (int w = w0 + lane; w <= w1; w += 32) M = fmaxf(M, p.part_ml[2 * slot(w)]);
+  for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(p.part_ml + 2 * slot(i)));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   float ell = 0.f, acc[F];
 #pragma unroll
   for (int j = 0; j < F; ++j) acc[j] = 0.f;
 #pragma unroll 4
-  for (int w = w0 + warp; w <= w1; w += 4) {
-    const size_t s = slot(w);
-    const float a = join_weight(p.part_ml[2 * s], M);
-    ell = fmaf(p.part_ml[2 * s + 1], a, ell);
+  for (int i = warp; i < parts; i += 4) {
+    const size_t s = slot(i);
+    const float a = join_weight(__ldcg(p.part_ml + 2 * s), M);
+    ell = fmaf(__ldcg(p.part_ml + 2 * s + 1), a, ell);
     const float* src = p.part_o + s * D;
 #pragma unroll
-    for (int j = 0; j < F; ++j) acc[j] = fmaf(src[32 * j + lane], a, acc[j]);
+    for (int j = 0; j < F; ++j) acc[j] = fmaf(__ldcg(src + 32 * j + lane), a, acc[j]);
   }
 #pragma unroll
   for (int j = 0; j < F; ++j) s_o[warp][32 * j + lane] = acc[j];
@@ -1029,6 +1045,7 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p
   __syncthreads();
   ell = s_l[0] + s_l[1] + s_l[2] + s_l[3];
   const float inv = ell == 0.f ? 0.f : 1.f / ell;
+  const size_t row = paged_row(p, unit.x, unit.y, unit.z + r);
   for (int f = threadIdx.x; f < D; f += 128)
     store_out<D, BF16>(p.o, row * D + f, (s_o[0][f] + s_o[1][f] + s_o[2][f] + s_o[3][f]) * inv);
   if (threadIdx.x == 0) p.lse[row] = ell == 0.f ? -INFINITY : (M + log2f(ell)) * 0.69314718055994531f;
@@ -1043,9 +1060,10 @@ static int paged_workers(int B, int Hk, int tiles, int Nk, int granule, int per_
   return (int)std::min<long long>(most, (long long)kSmCount * per_sm);
 }
 
-void paged_workspace(int B, int Nq, int H, int Hk, int Nk, int d, size_t* o_bytes, size_t* ml_bytes) {
+void paged_workspace(int B, int Nq, int H, int Hk, int Nk, int d, size_t* o_bytes, size_t* ml_bytes, size_t* unit_bytes) {
   const int R = H / Hk * Nq, rows = paged_tile_rows(R), tiles = (R + rows - 1) / rows;
-  const size_t slots = (size_t)2 * paged_workers(B, Hk, tiles, Nk, granule_keys(false), 4) * rows;
+  const size_t workers = paged_workers(B, Hk, tiles, Nk, granule_keys(false), 4), slots = 2 * workers * rows;
+  *unit_bytes = workers * sizeof(int4);
   *o_bytes = slots * d * sizeof(float);
   *ml_bytes = slots * 2 * sizeof(float);
 }
@@ -1061,9 +1079,9 @@ static cudaError_t launch_paged_v(PagedParams p, int B, int Nk, cudaStream_t str
   fa_paged_split_kernel<D, BF16, Q4, NT><<<p.workers, kPagedThreads, Cfg::kSmem, stream>>>(p);
   e = cudaPeekAtLastError();
   if (e != cudaSuccess) return e;
-  // the merge may start its index arithmetic while the last runs end; it waits for them before it reads a part
+  // the merge is launched while the runs end; it waits for them before it reads
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((size_t)B * p.Nq * p.H));
+  cfg.gridDim = dim3((unsigned)p.workers, 8 * NT);
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1071,7 +1089,7 @@ static cudaError_t launch_paged_v(PagedParams p, int B, int Nk, cudaStream_t str
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<D, BF16>, p, 8 * NT);
+  return cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<D, BF16>, p);
 }
 
 template <int D, bool BF16>
@@ -1088,6 +1106,7 @@ cudaError_t launch_decode_paged(const PagedDecodeArgs& a, const PagedArgs& pg, c
   p.lse = a.lse;
   p.part_o = a.part_o;
   p.part_ml = a.part_ml;
+  p.units = static_cast<int4*>(a.units);
   p.pg = pg;
   p.Nq = a.Nq;
   p.H = a.H;

@@ -77,11 +77,12 @@ static int set_paged(PagedArgs* p, const void* k_cache, const void* v_cache, con
 
 static size_t qk_bwd_workspace(int d) { return align256((size_t)2 * kQkBwdBlocks * d * sizeof(float)); }
 
-static size_t decode_paged_workspace(int B, int Nq, int H, int Hk, int Nk, int d, size_t* ml_at) {
-  size_t o_bytes, ml_bytes;
-  paged_workspace(B, Nq, H, Hk, Nk, d, &o_bytes, &ml_bytes);
+static size_t decode_paged_workspace(int B, int Nq, int H, int Hk, int Nk, int d, size_t* ml_at, size_t* units_at) {
+  size_t o_bytes, ml_bytes, unit_bytes;
+  paged_workspace(B, Nq, H, Hk, Nk, d, &o_bytes, &ml_bytes, &unit_bytes);
   *ml_at = align256(o_bytes);
-  return *ml_at + align256(ml_bytes);
+  *units_at = *ml_at + align256(ml_bytes);
+  return *units_at + align256(unit_bytes);
 }
 
 }  // namespace fa
@@ -222,8 +223,8 @@ static bool paged_sizes(int B, int Nq, int H, int Hk, int Nk, int d) {
 
 size_t fa_decode_paged_workspace_bytes(int B, int Nq, int H, int Hk, int Nk, int d) {
   if (!paged_sizes(B, Nq, H, Hk, Nk, d)) return 0;
-  size_t ml_at;
-  return decode_paged_workspace(B, Nq, H, Hk, Nk, d, &ml_at);
+  size_t ml_at, units_at;
+  return decode_paged_workspace(B, Nq, H, Hk, Nk, d, &ml_at, &units_at);
 }
 
 int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse, const int32_t* page_table,
@@ -238,12 +239,12 @@ int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, voi
   if (!paged_sizes(B, Nq, H, Hk, Nk, d)) return FA_ERR_UNSUPPORTED;
   const long long rows = (long long)(H / Hk) * Nq;
   if (B > 65535 || rows > 0x3fffffffLL || (rows + 15) / 16 * Hk > 65535) return FA_ERR_UNSUPPORTED;  // grid y, z
-  size_t ml_at;
-  const size_t need = decode_paged_workspace(B, Nq, H, Hk, Nk, d, &ml_at);
+  size_t ml_at, units_at;
+  const size_t need = decode_paged_workspace(B, Nq, H, Hk, Nk, d, &ml_at, &units_at);
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes_ < need)
     return FA_ERR_INVALID_ARG;
-  const PagedDecodeArgs a = {q, o, lse, reinterpret_cast<float*>(workspace),
-                             reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + ml_at), Nq, H, Nk, scale};
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const PagedDecodeArgs a = {q, o, lse, reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + ml_at), ws + units_at, Nq, H, Nk, scale};
   return map_launch(launch_decode_paged(a, pg, reinterpret_cast<cudaStream_t>(stream)));
 }
 
