@@ -87,29 +87,29 @@ struct PagedParams {
 template <bool BF16>
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (BF16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // The same with a zero sum to start from.
 __device__ __forceinline__ void mma_16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // 16 × 8 × 8 with a zero sum to start from.
 __device__ __forceinline__ void mma_1688_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
                : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3]) : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 
 // Transpose of an 8×8 matrix of 16-bit elements: lane (g, t) gives row g, columns 2t, 2t+1 and gets the same of the transpose.
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 
@@ -510,6 +510,7 @@ template <int D, bool BF16, int NT>
 struct Rows4 {
   static constexpr int W = D / 32, KS = D / 16, ROW = D / 2, PAIR = D / 8;
   static constexpr bool kCentre = NT == 1;  // −8·ΣP as a product
+  static constexpr int NS = 2;  // sub-tiles in flight together
   static constexpr float kDepth = 7.f;      // the reference is 2^7 under the maximum
   uint32_t qb[NT][KS][2], qs[NT];
   float m[NT][2], mz[NT][2], rise_at[NT][2];
@@ -597,6 +598,13 @@ struct Rows4 {
     }
   }
 
+  static __device__ __forceinline__ float top_of(const float (&s)[NS][NT][4], int nt, int u) {
+    float x = fmaxf(s[0][nt][u], s[0][nt][2 + u]);
+#pragma unroll
+    for (int ns = 1; ns < NS; ++ns) x = max3f(x, s[ns][nt][u], s[ns][nt][2 + u]);
+    return x;
+  }
+
   __device__ __forceinline__ void step(uint32_t tile, int j0, uint32_t flags) {
     const bool special = j0 + 32 > L || flags != 3u;  // some keys are not there
     auto live = [&](int sub, int key) { return ((flags >> sub) & 1u) != 0u && j0 + 16 * sub + key < L; };
@@ -626,10 +634,18 @@ struct Rows4 {
       for (int j = 1; j < W; ++j) top = __hmax2(top, *reinterpret_cast<const __half2*>(&w[j]));
       most = __low2float(top);
     }
-    // ---- scores of keys j0 + 16·sub + g and + 8
-    float s[2][NT][4];
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
+    for (int sub0 = 0; sub0 < 2; sub0 += NS) part(tile, j0, flags, special, most, sub0);
+  }
+
+  // Sub-tiles sub0 … sub0 + NS − 1.
+  __device__ __forceinline__ void part(uint32_t tile, int j0, uint32_t flags, bool special, float most, const int sub0) {
+    auto live = [&](int sub, int key) { return ((flags >> sub) & 1u) != 0u && j0 + 16 * sub + key < L; };
+    // ---- scores of keys j0 + 16·sub + g and + 8
+    float s[NS][NT][4];
+#pragma unroll
+    for (int ns = 0; ns < NS; ++ns) {
+      const int sub = sub0 + ns;
       uint32_t kn[2][W], kp[2][W], mn[2];
       const uint32_t ak = tile + lane_k + sub * 16 * ROW, ap = tile + lane_p + sub * 16 * PAIR, am = tile + lane_m + sub * 16 * PAIR;
       if constexpr (W == 4) {
@@ -653,7 +669,7 @@ struct Rows4 {
         float acc[4];
         mma_1688_first(acc, mn[0], mn[1], qs[nt]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[sub][nt][i] = acc[i] * 9.5367431640625e-07f;  // 2^-20: from 2^(8 − e) to 2^-(e + 12)
+        for (int i = 0; i < 4; ++i) s[ns][nt][i] = acc[i] * 9.5367431640625e-07f;  // 2^-20: from 2^(8 − e) to 2^-(e + 12)
       }
 #pragma unroll
       for (int j = 0; j < W; ++j) {
@@ -666,23 +682,23 @@ struct Rows4 {
           mma_16816_first(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qb[nt][2 * j][0], qb[nt][2 * j][1]);
           mma_16816<false>(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qb[nt][2 * j + 1][0],
                            qb[nt][2 * j + 1][1]);
-          s[sub][nt][0] = fmaf(p0, acc[0], s[sub][nt][0]);
-          s[sub][nt][1] = fmaf(p0, acc[1], s[sub][nt][1]);
-          s[sub][nt][2] = fmaf(p1, acc[2], s[sub][nt][2]);
-          s[sub][nt][3] = fmaf(p1, acc[3], s[sub][nt][3]);
+          s[ns][nt][0] = fmaf(p0, acc[0], s[ns][nt][0]);
+          s[ns][nt][1] = fmaf(p0, acc[1], s[ns][nt][1]);
+          s[ns][nt][2] = fmaf(p1, acc[2], s[ns][nt][2]);
+          s[ns][nt][3] = fmaf(p1, acc[3], s[ns][nt][3]);
         }
       }
     }
     // ---- keys behind a row's last one, or that are not there: they may hold anything, so they are replaced
     if (special || j0 + 31 > L - Nq) {
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub)
+      for (int ns = 0; ns < NS; ++ns)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int key = g + 8 * (i >> 1);
-            if (!live(sub, key) || j0 + 16 * sub + key > lim[nt][i & 1]) s[sub][nt][i] = -INFINITY;
+            const int key = g + 8 * (i >> 1), sub = sub0 + ns;
+            if (!live(sub, key) || j0 + 16 * sub + key > lim[nt][i & 1]) s[ns][nt][i] = -INFINITY;
           }
     }
     // ---- the reference (NaN does not raise it: it reaches the sums all the same)
@@ -691,7 +707,7 @@ struct Rows4 {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        rise = rise || fmaxf(fmaxf(s[0][nt][u], s[0][nt][2 + u]), fmaxf(s[1][nt][u], s[1][nt][2 + u])) > rise_at[nt][u];
+        rise = rise || top_of(s, nt, u) > rise_at[nt][u];
     if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
@@ -700,7 +716,7 @@ struct Rows4 {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          float x = fmaxf(fmaxf(s[0][nt][u], s[0][nt][2 + u]), fmaxf(s[1][nt][u], s[1][nt][2 + u]));
+          float x = top_of(s, nt, u);
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
           // m is the reference: 2^(7 − cap) under the largest score when it was set
@@ -721,14 +737,15 @@ struct Rows4 {
       cap_value = exp2f(next);
     }
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
+    for (int ns = 0; ns < NS; ++ns) {
+      const int sub = sub0 + ns;
       // ---- probabilities (up to 2^(15 − cap)), rounded to fp16 and transposed
       uint32_t bh[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float pr[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pr[i] = ex2(fmaf(s[sub][nt][i], coef[nt][i & 1], -mz[nt][i & 1]));
+        for (int i = 0; i < 4; ++i) pr[i] = ex2(fmaf(s[ns][nt][i], coef[nt][i & 1], -mz[nt][i & 1]));
         l[nt][0] += pr[0] + pr[2];
         l[nt][1] += pr[1] + pr[3];
 #pragma unroll
