@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_append_kernel(const Ap
   if (page < 0) return;
   const RopeLane rl = rope_lane<INTER>(l, ra.rot_dim);
   float cs[8], sn[8];
-  if (!rope_angles(ra, t, a.T, at, rl, cs, sn)) return;
+  if (!rope_angles(ra, rope_positions(ra, t, a.T, at, rl), rl, cs, sn)) return;
   const int gq = (a.Hq + RPW - 1) / RPW, gk = (pg.Hk + RPW - 1) / RPW;
 #pragma unroll 1
   for (int gi = blockIdx.y; gi < gq + 2 * gk; gi += gridDim.y) {

@@ -98,6 +98,22 @@ struct DecodeArgs {
   float* part_ml;  // [B·H, chunks, 2] fp32
 };
 
+// Launches a kernel that may be scheduled while the one before it in the stream ends (programmatic dependent launch);
+// it waits for that one itself (griddepcontrol.wait) before it reads what it wrote.
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The grid rules' number of SMs (B200).
 constexpr int kSmCount = 148;
 
@@ -126,7 +142,7 @@ struct QkArgs {
   int T, Hq, Hk;
   float eps;
 };
-constexpr int kQkBwdBlocks = 296;  // at most, for the queries and for the keys
+constexpr int kQkBwdBlocks = 2 * kSmCount;  // at most, for the queries and the keys together
 struct QkBwdArgs {
   const void* dq_out;
   const void* dk_out;

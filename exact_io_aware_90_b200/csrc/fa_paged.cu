@@ -191,9 +191,6 @@ __device__ __forceinline__ void store_out(void* o, size_t at, float v) {
   else reinterpret_cast<__half*>(o)[at] = __float2half_rn(v);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 // Shared-memory loads at a 32-bit address plus a constant.
 template <int OFF>
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -223,11 +220,6 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Places of 16-byte pieces in shared memory (c: piece of row r), such that the pieces one shared-memory access reads
@@ -1097,16 +1089,7 @@ static cudaError_t launch_paged_v(PagedParams p, int B, int Nk, cudaStream_t str
   e = cudaPeekAtLastError();
   if (e != cudaSuccess) return e;
   // the merge is launched while the runs end; it waits for them before it reads
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.workers, 8 * NT);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<D, BF16>, p);
+  return launch_after(fa_paged_merge_kernel<D, BF16>, dim3((unsigned)p.workers, 8 * NT), dim3(128), stream, p);
 }
 
 template <int D, bool BF16>

@@ -75,7 +75,7 @@ static int set_paged(PagedArgs* p, const void* k_cache, const void* v_cache, con
   return FA_OK;
 }
 
-static size_t qk_bwd_workspace(int d) { return align256((size_t)2 * kQkBwdBlocks * d * sizeof(float)); }
+static size_t qk_bwd_workspace(int d) { return align256((size_t)kQkBwdBlocks * d * sizeof(float)); }
 
 static size_t decode_paged_workspace(int B, int Nq, int H, int Hk, int Nk, int d, size_t* ml_at, size_t* units_at) {
   size_t o_bytes, ml_bytes, unit_bytes;

@@ -16,6 +16,8 @@
 namespace fa {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeStages = 4;  // of the backward's ring: 80 KB in flight per block, two blocks per SM
+constexpr int kRopeRing = kRopeThreads / 32 * kRopeStages * 4 * 32 * 16;
 
 // ---------------------------------------------------------------- table
 // cos and sin of p·base^(−2i/rot) in 64 bits: an fp32 angle would be off by 2^-24·p radians at position p.
@@ -38,46 +40,59 @@ __device__ __forceinline__ void load_weights(const void* w, const RopeLane& rl, 
   unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(p + 2 * rl.c1)), x + 8);
 }
 
-template <int D, bool BF16, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) fa_qk_norm_rope_kernel(const QkArgs a, const RopeArgs ra) {
+// U: row groups (of 512/d rows) that a warp loads before it works on the first.
+template <int D, bool BF16, bool INTER, int U>
+__global__ void __launch_bounds__(kRopeThreads, 3) fa_qk_norm_rope_kernel(const QkArgs a, const RopeArgs ra) {
   constexpr int G = D / 16, RPW = 32 / G;  // lanes per row, rows per warp at a time
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * (kRopeThreads / 32) + warp;
   if (t >= a.T) return;
   const RopeLane rl = rope_lane<INTER>(lane % G, ra.rot_dim);
   float cs[8], sn[8];
-  if (!rope_angles(ra, t, a.T, 0, rl, cs, sn)) return;
+  if (!rope_angles(ra, rope_positions(ra, t, a.T, 0, rl), rl, cs, sn)) return;
 #pragma unroll 1
   for (int part = 0; part < 2; ++part) {
     const int H = part == 0 ? a.Hq : a.Hk;
     const uint8_t* src = static_cast<const uint8_t*>(part == 0 ? a.q : a.k) + (size_t)t * (part == 0 ? a.q_stride : a.k_stride) * 2;
     uint8_t* dst = static_cast<uint8_t*>(part == 0 ? a.q_out : a.k_out) + (size_t)t * (part == 0 ? a.q_out_stride : a.k_out_stride) * 2;
     const void* wp = part == 0 ? a.wq : a.wk;
-    float w[16];
-    if (wp != nullptr) load_weights<D, BF16>(wp, rl, w);
+    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;  // the weights stay packed: unpacking costs less than the registers
+    if (wp != nullptr) {
+      w0 = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + 2 * rl.c0));
+      w1 = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + 2 * rl.c1));
+    }
 #pragma unroll 1
-    for (int h0 = blockIdx.y * RPW; h0 < H; h0 += gridDim.y * RPW) {
+    for (int h0 = blockIdx.y * (RPW * U); h0 < H; h0 += gridDim.y * (RPW * U)) {
       const int h = h0 + lane / G;
-      const bool on = h < H;
-      float x[16];
-      if (on) {
-        const uint8_t* p = src + (size_t)h * D * 2;
-        unpack8<BF16>(*reinterpret_cast<const uint4*>(p + 2 * rl.c0), x);
-        unpack8<BF16>(*reinterpret_cast<const uint4*>(p + 2 * rl.c1), x + 8);
-      } else {
+      uint4 v0[U], v1[U];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = 0.f;
+      for (int u = 0; u < U; ++u) {
+        v0[u] = v1[u] = make_uint4(0, 0, 0, 0);
+        if (h + u * RPW < H) {
+          const uint8_t* p = src + (size_t)(h + u * RPW) * D * 2;
+          v0[u] = __ldcs(reinterpret_cast<const uint4*>(p + 2 * rl.c0));
+          v1[u] = __ldcs(reinterpret_cast<const uint4*>(p + 2 * rl.c1));
+        }
       }
-      if (wp != nullptr) {
-        const float r = row_rms_inv<D>(x, a.eps);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
-      }
-      if (rl.rot) rope_rotate<INTER, false>(x, cs, sn);
-      if (on) {
-        uint8_t* p = dst + (size_t)h * D * 2;
-        *reinterpret_cast<uint4*>(p + 2 * rl.c0) = pack8<BF16>(x);
-        *reinterpret_cast<uint4*>(p + 2 * rl.c1) = pack8<BF16>(x + 8);
+      for (int u = 0; u < U; ++u) {
+        float x[16];
+        unpack8<BF16>(v0[u], x);
+        unpack8<BF16>(v1[u], x + 8);
+        if (wp != nullptr) {
+          const float r = row_rms_inv<D>(x, a.eps);
+          float w[16];
+          unpack8<BF16>(w0, w);
+          unpack8<BF16>(w1, w + 8);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
+        }
+        if (rl.rot) rope_rotate<INTER, false>(x, cs, sn);
+        if (h + u * RPW < H) {
+          uint8_t* p = dst + (size_t)(h + u * RPW) * D * 2;
+          __stcs(reinterpret_cast<uint4*>(p + 2 * rl.c0), pack8<BF16>(x));
+          __stcs(reinterpret_cast<uint4*>(p + 2 * rl.c1), pack8<BF16>(x + 8));
+        }
       }
     }
   }
@@ -85,8 +100,9 @@ __global__ void __launch_bounds__(kRopeThreads) fa_qk_norm_rope_kernel(const QkA
 
 // ---------------------------------------------------------------- backward
 template <int D, bool BF16, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) fa_qk_norm_rope_bwd_kernel(const QkBwdArgs a, const RopeArgs ra) {
+__global__ void __launch_bounds__(kRopeThreads, 2) fa_qk_norm_rope_bwd_kernel(const QkBwdArgs a, const RopeArgs ra) {
   constexpr int G = D / 16, RPW = 32 / G, WARPS = kRopeThreads / 32;
+  extern __shared__ __align__(16) uint4 s_ring[];  // [warps][stages][4 pieces][lanes]
   __shared__ float s_dw[WARPS][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool isk = (int)blockIdx.x >= a.q_blocks;  // the first q_blocks blocks take the queries
@@ -98,51 +114,87 @@ __global__ void __launch_bounds__(kRopeThreads) fa_qk_norm_rope_bwd_kernel(const
   const long long gs = isk ? a.gk_stride : a.gq_stride, xs = isk ? a.k_stride : a.q_stride, ds = isk ? a.dk_stride : a.dq_stride;
   const void* wp = isk ? a.wk : a.wq;
   const RopeLane rl = rope_lane<INTER>(lane % G, ra.rot_dim);
-  float w[16], dw[16];
-  if (wp != nullptr) load_weights<D, BF16>(wp, rl, w);
+  uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+  if (wp != nullptr) {
+    w0 = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + 2 * rl.c0));
+    w1 = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + 2 * rl.c1));
+  }
+  float dw[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) dw[i] = 0.f;
-#pragma unroll 1
-  for (int t = blk * WARPS + warp; t < a.T; t += nblk * WARPS) {
-    float cs[8], sn[8];
-    if (!rope_angles(ra, t, a.T, 0, rl, cs, sn)) continue;
-#pragma unroll 1
-    for (int h0 = 0; h0 < H; h0 += RPW) {
-      const int h = h0 + lane / G;
-      const bool on = h < H;
-      float g[16], x[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) g[i] = x[i] = 0.f;
-      if (on) {
-        const uint8_t* p = gy + ((size_t)t * gs + (size_t)h * D) * 2;
-        unpack8<BF16>(*reinterpret_cast<const uint4*>(p + 2 * rl.c0), g);
-        unpack8<BF16>(*reinterpret_cast<const uint4*>(p + 2 * rl.c1), g + 8);
-        if (wp != nullptr) {
-          const uint8_t* px = xx + ((size_t)t * xs + (size_t)h * D) * 2;
-          unpack8<BF16>(*reinterpret_cast<const uint4*>(px + 2 * rl.c0), x);
-          unpack8<BF16>(*reinterpret_cast<const uint4*>(px + 2 * rl.c1), x + 8);
-        }
-      }
-      if (rl.rot) rope_rotate<INTER, true>(g, cs, sn);
+  // Each lane copies the pieces of its own rows ahead into its own places of the ring, so that no other thread is waited
+  // for: the copies in flight, 2 KB a group, do not take registers.
+  uint4* mine = s_ring + warp * (kRopeStages * 4 * 32) + lane;
+  int t = blk * WARPS + warp, h0 = 0, t_next = t, h_next = 0, stage = 0, stage_next = 0;
+  auto issue = [&]() {
+    const int h = h_next + lane / G;
+    if (t_next < a.T && h < H) {
+      const uint32_t to = smem_u32(mine + stage_next * 128);
+      const uint8_t* p = gy + ((size_t)t_next * gs + (size_t)h * D) * 2;
+      cp_async16(to, p + 2 * rl.c0);
+      cp_async16(to + 512, p + 2 * rl.c1);
       if (wp != nullptr) {
-        const float r = row_rms_inv<D>(x, a.eps);
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          x[i] *= r;
-          dw[i] = fmaf(g[i], x[i], dw[i]);
-          g[i] *= w[i];
-          dot = fmaf(g[i], x[i], dot);
-        }
-        dot = row_sum<D>(dot) * (1.f / D);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) g[i] = r * (g[i] - x[i] * dot);
+        const uint8_t* px = xx + ((size_t)t_next * xs + (size_t)h * D) * 2;
+        cp_async16(to + 1024, px + 2 * rl.c0);
+        cp_async16(to + 1536, px + 2 * rl.c1);
       }
-      if (on) {
-        uint8_t* p = dx + ((size_t)t * ds + (size_t)h * D) * 2;
-        *reinterpret_cast<uint4*>(p + 2 * rl.c0) = pack8<BF16>(g);
-        *reinterpret_cast<uint4*>(p + 2 * rl.c1) = pack8<BF16>(g + 8);
+    }
+    cp_async_commit();
+    stage_next = stage_next + 1 == kRopeStages ? 0 : stage_next + 1;
+    h_next += RPW;
+    if (h_next >= H) {
+      h_next = 0;
+      t_next += nblk * WARPS;
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kRopeStages - 1; ++s) issue();
+  float cs[8], sn[8];
+  bool ok = true;
+  int2 pos = t < a.T ? rope_positions(ra, t, a.T, 0, rl) : make_int2(0, 0);
+#pragma unroll 1
+  while (t < a.T) {
+    if (h0 == 0) ok = rope_angles(ra, pos, rl, cs, sn);
+    const int t_now = t, h = h0 + lane / G;
+    h0 += RPW;
+    if (h0 >= H) {
+      h0 = 0;
+      t += nblk * WARPS;
+      if (t < a.T) pos = rope_positions(ra, t, a.T, 0, rl);
+    }
+    cp_async_wait<kRopeStages - 2>();
+    const uint4* from = mine + stage * 128;
+    stage = stage + 1 == kRopeStages ? 0 : stage + 1;
+    float g[16], x[16];
+    const bool on = h < H;
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    unpack8<BF16>(on ? from[0] : none, g);
+    unpack8<BF16>(on ? from[32] : none, g + 8);
+    unpack8<BF16>(on && wp != nullptr ? from[64] : none, x);
+    unpack8<BF16>(on && wp != nullptr ? from[96] : none, x + 8);
+    issue();  // into the place that the last turn read
+    if (!ok) continue;  // a position out of range: the token is left out
+    if (rl.rot) rope_rotate<INTER, true>(g, cs, sn);
+    if (wp != nullptr) {
+      const float r = row_rms_inv<D>(x, a.eps);
+      float dot = 0.f, w[16];
+      unpack8<BF16>(w0, w);
+      unpack8<BF16>(w1, w + 8);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x[i] *= r;
+        dw[i] = fmaf(g[i], x[i], dw[i]);
+        g[i] *= w[i];
+        dot = fmaf(g[i], x[i], dot);
       }
+      dot = row_sum<D>(dot) * (1.f / D);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) g[i] = r * (g[i] - x[i] * dot);
+    }
+    if (on) {
+      uint8_t* p = dx + ((size_t)t_now * ds + (size_t)h * D) * 2;
+      __stcs(reinterpret_cast<uint4*>(p + 2 * rl.c0), pack8<BF16>(g));
+      __stcs(reinterpret_cast<uint4*>(p + 2 * rl.c1), pack8<BF16>(g + 8));
     }
   }
   if (wp == nullptr) return;
@@ -174,8 +226,10 @@ __global__ void __launch_bounds__(1024) fa_qk_norm_rope_dw_kernel(const float* p
   const bool isk = blockIdx.y != 0;
   const int first = isk ? q_blocks : 0, n = isk ? k_blocks : q_blocks;
   const int f = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float v = 0.f;
-  for (int b = slice; b < n; b += 32) v += part[(size_t)(first + b) * d + f];
+#pragma unroll 4
+  for (int b = slice; b < n; b += 32) v += __ldcg(part + (size_t)(first + b) * d + f);
   s[slice][threadIdx.x & 31] = v;
   __syncthreads();
   if (slice == 0) {
@@ -187,17 +241,21 @@ __global__ void __launch_bounds__(1024) fa_qk_norm_rope_dw_kernel(const float* p
 }
 
 // ---------------------------------------------------------------- launches
+template <int D, bool BF16, int U>
+static cudaError_t launch_qk_u(const QkArgs& a, const RopeArgs& ra, int blocks, cudaStream_t stream) {
+  const int most = (max(a.Hq, a.Hk) + 512 / D * U - 1) / (512 / D * U);
+  const dim3 grid(blocks, max(1, min(most, 2 * kSmCount / blocks)));  // few tokens: the heads are spread over blocks too
+  if (ra.interleaved) fa_qk_norm_rope_kernel<D, BF16, true, U><<<grid, kRopeThreads, 0, stream>>>(a, ra);
+  else fa_qk_norm_rope_kernel<D, BF16, false, U><<<grid, kRopeThreads, 0, stream>>>(a, ra);
+  return cudaPeekAtLastError();
+}
+
+// Two row groups ahead where the blocks fill the GPU (32768 tokens x 32 heads, d = 128: 89.6 us against 110.7 with one
+// and 101 with four); one where they do not, so that there are more of them (1171 tokens: 3.7 us against 4.1).
 template <int D, bool BF16>
 static cudaError_t launch_qk_t(const QkArgs& a, const RopeArgs& ra, cudaStream_t stream) {
-  constexpr int RPW = 512 / D;
   const int blocks = (a.T + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  const int most = (max(a.Hq, a.Hk) + RPW - 1) / RPW;
-  // few tokens: spread the heads over blocks too, up to one row group each
-  const int split = max(1, min(most, 2 * kSmCount / blocks));
-  const dim3 grid(blocks, split);
-  if (ra.interleaved) fa_qk_norm_rope_kernel<D, BF16, true><<<grid, kRopeThreads, 0, stream>>>(a, ra);
-  else fa_qk_norm_rope_kernel<D, BF16, false><<<grid, kRopeThreads, 0, stream>>>(a, ra);
-  return cudaPeekAtLastError();
+  return blocks >= 2 * kSmCount ? launch_qk_u<D, BF16, 2>(a, ra, blocks, stream) : launch_qk_u<D, BF16, 1>(a, ra, blocks, stream);
 }
 
 cudaError_t launch_qk_norm_rope(const QkArgs& a, const RopeArgs& ra, int d, bool bf16, cudaStream_t stream) {
@@ -205,19 +263,21 @@ cudaError_t launch_qk_norm_rope(const QkArgs& a, const RopeArgs& ra, int d, bool
   return bf16 ? launch_qk_t<64, true>(a, ra, stream) : launch_qk_t<64, false>(a, ra, stream);
 }
 
-// Blocks for the queries and for the keys: at most kQkBwdBlocks of each, a warp per token at least.
-static int qk_bwd_side_blocks(int T) { return max(1, min(kQkBwdBlocks, (T + kRopeThreads / 32 - 1) / (kRopeThreads / 32))); }
-
+// One wave of blocks (two per SM), shared between the queries and the keys by their heads; a warp per token at least.
 template <int D, bool BF16>
 static cudaError_t launch_qk_bwd_t(QkBwdArgs a, const RopeArgs& ra, cudaStream_t stream) {
-  const int side = qk_bwd_side_blocks(a.T);
-  a.q_blocks = side;
-  if (ra.interleaved) fa_qk_norm_rope_bwd_kernel<D, BF16, true><<<2 * side, kRopeThreads, 0, stream>>>(a, ra);
-  else fa_qk_norm_rope_bwd_kernel<D, BF16, false><<<2 * side, kRopeThreads, 0, stream>>>(a, ra);
-  cudaError_t e = cudaPeekAtLastError();
+  const int most = max(1, (a.T + kRopeThreads / 32 - 1) / (kRopeThreads / 32));
+  const int share = (int)((long long)kQkBwdBlocks * a.Hq / (a.Hq + a.Hk));
+  a.q_blocks = min(most, max(1, min(kQkBwdBlocks - 1, share)));
+  const int k_blocks = min(most, kQkBwdBlocks - max(1, min(kQkBwdBlocks - 1, share)));
+  auto kernel = ra.interleaved ? fa_qk_norm_rope_bwd_kernel<D, BF16, true> : fa_qk_norm_rope_bwd_kernel<D, BF16, false>;
+  static std::atomic<unsigned long long> done[2] = {{0}, {0}};
+  cudaError_t e = set_smem_once(done[ra.interleaved], reinterpret_cast<const void*>(kernel), kRopeRing);
+  if (e != cudaSuccess) return e;
+  kernel<<<a.q_blocks + k_blocks, kRopeThreads, kRopeRing, stream>>>(a, ra);
+  e = cudaPeekAtLastError();
   if (e != cudaSuccess || a.wq == nullptr) return e;
-  fa_qk_norm_rope_dw_kernel<<<dim3(D / 32, 2), 1024, 0, stream>>>(a.part, a.dwq, a.dwk, side, side, D);
-  return cudaPeekAtLastError();
+  return launch_after(fa_qk_norm_rope_dw_kernel, dim3(D / 32, 2), dim3(1024), stream, (const float*)a.part, a.dwq, a.dwk, a.q_blocks, k_blocks, D);
 }
 
 cudaError_t launch_qk_norm_rope_bwd(const QkBwdArgs& a, const RopeArgs& ra, int d, bool bf16, cudaStream_t stream) {

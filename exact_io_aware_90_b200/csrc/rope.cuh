@@ -38,26 +38,26 @@ __device__ __forceinline__ RopeLane rope_lane(int l, int rot_dim) {
   return r;
 }
 
-// cos and sin of this lane's eight frequencies for token t.  Frequency i goes by the position of the
-// axis whose section holds i (sections are multiples of 4, so a 16-byte load lies in one).  False, with
-// the status recorded, when a position is outside the table.  pos0 >= 0 stands for positions == nullptr.
-__device__ __forceinline__ bool rope_angles(const RopeArgs& ra, int t, int T, int pos0, const RopeLane& rl, float (&cs)[8],
-                                            float (&sn)[8]) {
-  if (ra.cos_t == nullptr) return true;  // no rotation at all
-  bool ok = true;
-  int pos[2];
+// The positions that this lane's eight frequencies of token t go by, four by four: frequency i goes by the axis whose
+// section holds i (sections are multiples of 4).  pos0 stands for positions == nullptr.
+__device__ __forceinline__ int2 rope_positions(const RopeArgs& ra, int t, int T, int pos0, const RopeLane& rl) {
+  if (ra.positions == nullptr) return make_int2(pos0, pos0);
+  int axis[2] = {0, 0};
+  if (ra.axes > 1) {
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    int axis = 0;
-    if (ra.axes > 1) {
-      const int f = rl.f0 + 4 * u;
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int a = 0; a < kRopeMaxAxes - 1; ++a) axis += (a + 1 < ra.axes && f >= ra.section_end[a]) ? 1 : 0;
-    }
-    pos[u] = ra.positions != nullptr ? __ldg(ra.positions + (size_t)axis * T + t) : pos0;
-    ok = ok && (pos[u] >= 0 && pos[u] < ra.table_rows);
+      for (int a = 0; a < kRopeMaxAxes - 1; ++a) axis[u] += (a + 1 < ra.axes && rl.f0 + 4 * u >= ra.section_end[a]) ? 1 : 0;
   }
-  if (!rl.rot) ok = true;  // this lane reads no table row
+  const int first = __ldg(ra.positions + (size_t)axis[0] * T + t);
+  return make_int2(first, axis[1] == axis[0] ? first : __ldg(ra.positions + (size_t)axis[1] * T + t));
+}
+
+// cos and sin of this lane's eight frequencies.  False, with the status recorded, when a position that the warp's lanes
+// read with is outside the table.
+__device__ __forceinline__ bool rope_angles(const RopeArgs& ra, int2 pos, const RopeLane& rl, float (&cs)[8], float (&sn)[8]) {
+  if (ra.cos_t == nullptr) return true;  // no rotation at all
+  const bool ok = !rl.rot || ((unsigned)pos.x < (unsigned)ra.table_rows && (unsigned)pos.y < (unsigned)ra.table_rows);
   if (!__all_sync(0xffffffffu, ok)) {
     if (lane_id() == 0) record_status(1);
     return false;
@@ -65,7 +65,7 @@ __device__ __forceinline__ bool rope_angles(const RopeArgs& ra, int t, int T, in
   if (rl.rot) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const size_t at = (size_t)pos[u] * (ra.rot_dim / 2) + rl.f0 + 4 * u;
+      const size_t at = (size_t)(u ? pos.y : pos.x) * (ra.rot_dim / 2) + rl.f0 + 4 * u;
       const float4 c = __ldg(reinterpret_cast<const float4*>(ra.cos_t + at));
       const float4 s = __ldg(reinterpret_cast<const float4*>(ra.sin_t + at));
       cs[4 * u] = c.x; cs[4 * u + 1] = c.y; cs[4 * u + 2] = c.z; cs[4 * u + 3] = c.w;
