@@ -37,104 +37,159 @@ __device__ __forceinline__ bool owner_of(const int32_t* cu, int B, int T, int t,
   return true;
 }
 
+// The work is dealt out as units of 512/d rows: for each token the groups of its query heads, of its key heads, of its
+// value heads.  A warp takes a run of units, so few tokens spread over as many warps as there are units, and many tokens
+// keep their lookups and angles for a dozen units.  The rows come ahead through a ring in shared memory; each lane copies
+// the pieces it will read itself, so nothing waits for another thread.
+constexpr int kCacheStages = 8;
+constexpr int kCacheRing = kCacheThreads / 32 * kCacheStages * 2 * 32 * 16;
+constexpr int kCacheBlocks = 3;  // per SM: 168 KB in flight
+
 template <int D, bool BF16, bool INTER, bool Q4>
-__global__ void __launch_bounds__(kCacheThreads) fa_cache_append_kernel(const AppendArgs a, const RopeArgs ra, const PagedArgs pg) {
+__global__ void __launch_bounds__(kCacheThreads, kCacheBlocks) fa_cache_append_kernel(const AppendArgs a, const RopeArgs ra,
+                                                                                      const PagedArgs pg, int share) {
   constexpr int G = D / 16, RPW = 32 / G, W = D / 32;
+  extern __shared__ __align__(16) uint4 s_ring[];                      // [warps][stages][2 pieces][lanes]
   __shared__ uint4 s_rows[Q4 ? kCacheThreads / 32 : 1][Q4 ? 64 : 1];  // a warp's rows, 512 values
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G;
-  const int t = blockIdx.x * (kCacheThreads / 32) + warp;
-  if (t >= a.T) return;
-  int b, i, n;
-  if (!owner_of(a.cu_seqlens, pg.B, a.T, t, b, i, n)) return;
-  const int len = __ldg(pg.seqlens_k + b);
-  const int at = len - n + i;
-  int slot;
-  const int page = page_of(pg, b, len < n ? -1 : at, slot);
-  if (page < 0) return;
+  const int gq = (a.Hq + RPW - 1) / RPW, gk = (pg.Hk + RPW - 1) / RPW, groups = gq + 2 * gk;
+  const long long u0 = ((long long)blockIdx.x * (kCacheThreads / 32) + warp) * share, all = (long long)a.T * groups;
+  if (u0 >= all) return;
+  int left = (int)min((long long)share, all - u0), to_copy = left;
+  int t = (int)(u0 / groups), gi = (int)(u0 - (long long)t * groups);
   const RopeLane rl = rope_lane<INTER>(l, ra.rot_dim);
+  uint4* mine = s_ring + warp * (kCacheStages * 2 * 32) + lane;
+  int t_next = t, g_next = gi, stage = 0, stage_next = 0;
+  auto issue = [&]() {
+    if (to_copy > 0) {
+      --to_copy;
+      const int part = g_next < gq ? 0 : g_next < gq + gk ? 1 : 2;  // queries, keys, values
+      const int h = (part == 0 ? g_next : part == 1 ? g_next - gq : g_next - gq - gk) * RPW + lane / G;
+      if (h < (part == 0 ? a.Hq : pg.Hk)) {
+        const uint8_t* src = static_cast<const uint8_t*>(part == 0 ? a.q : part == 1 ? a.k : a.v) +
+                             ((size_t)t_next * (part == 0 ? a.q_stride : part == 1 ? a.k_stride : a.v_stride) + (size_t)h * D) * 2;
+        const uint32_t to = smem_u32(mine + stage_next * 64);
+        cp_async16(to, src + 2 * rl.c0);
+        cp_async16(to + 512, src + 2 * rl.c1);
+      }
+      if (++g_next == groups) {
+        g_next = 0;
+        ++t_next;
+      }
+    }
+    stage_next = stage_next + 1 == kCacheStages ? 0 : stage_next + 1;
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kCacheStages - 1; ++s) issue();
   float cs[8], sn[8];
-  if (!rope_angles(ra, rope_positions(ra, t, a.T, at, rl), rl, cs, sn)) return;
-  const int gq = (a.Hq + RPW - 1) / RPW, gk = (pg.Hk + RPW - 1) / RPW;
+  int page = -1, slot = 0;
+  bool fresh = true;  // the token's lookups are to be made
 #pragma unroll 1
-  for (int gi = blockIdx.y; gi < gq + 2 * gk; gi += gridDim.y) {
-    const int part = gi < gq ? 0 : gi < gq + gk ? 1 : 2;  // queries, keys, values
+  for (; left > 0; --left) {
+    if (fresh) {
+      fresh = false;
+      int b, i, n;
+      page = -1;
+      if (owner_of(a.cu_seqlens, pg.B, a.T, t, b, i, n)) {
+        const int len = __ldg(pg.seqlens_k + b);
+        const int at = len - n + i;
+        const int2 pos = rope_positions(ra, t, a.T, at, rl);
+        page = page_of(pg, b, len < n ? -1 : at, slot);
+        if (page >= 0 && !rope_angles(ra, pos, rl, cs, sn)) page = -1;
+      }
+    }
+    const int part = gi < gq ? 0 : gi < gq + gk ? 1 : 2, t_now = t;
     const int h = (part == 0 ? gi : part == 1 ? gi - gq : gi - gq - gk) * RPW + lane / G;
     const bool on = h < (part == 0 ? a.Hq : pg.Hk);
-    const uint8_t* src = static_cast<const uint8_t*>(part == 0 ? a.q : part == 1 ? a.k : a.v) +
-                         ((size_t)t * (part == 0 ? a.q_stride : part == 1 ? a.k_stride : a.v_stride) + (size_t)h * D) * 2;
-    uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
+    if (++gi == groups) {
+      gi = 0;
+      ++t;
+      fresh = true;
+    }
+    cp_async_wait<kCacheStages - 2>();
+    const uint4* from = mine + stage * 64;
+    stage = stage + 1 == kCacheStages ? 0 : stage + 1;
+    uint4 p0 = make_uint4(0, 0, 0, 0), p1 = p0;
     if (on) {
-      u0 = *reinterpret_cast<const uint4*>(src + 2 * rl.c0);
-      u1 = *reinterpret_cast<const uint4*>(src + 2 * rl.c1);
+      p0 = from[0];
+      p1 = from[32];
     }
-    const void* wp = part == 0 ? a.wq : part == 1 ? a.wk : nullptr;
-    if (part < 2 && (wp != nullptr || ra.cos_t != nullptr)) {
-      float x[16];
-      unpack8<BF16>(u0, x);
-      unpack8<BF16>(u1, x + 8);
-      if (wp != nullptr) {
-        const float r = row_rms_inv<D>(x, a.eps);
-        float w[16];
-        const uint8_t* p = static_cast<const uint8_t*>(wp);
-        unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(p + 2 * rl.c0)), w);
-        unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(p + 2 * rl.c1)), w + 8);
+    issue();  // into the place that the last turn read
+    if (page < 0) continue;  // no sequence's token, or one that cannot be placed
+    {
+      const void* wp = part == 0 ? a.wq : part == 1 ? a.wk : nullptr;
+      if (part < 2 && (wp != nullptr || ra.cos_t != nullptr)) {
+        float x[16];
+        unpack8<BF16>(p0, x);
+        unpack8<BF16>(p1, x + 8);
+        if (wp != nullptr) {
+          const float r = row_rms_inv<D>(x, a.eps);
+          float w[16];
+          const uint8_t* p = static_cast<const uint8_t*>(wp);
+          unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(p + 2 * rl.c0)), w);
+          unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(p + 2 * rl.c1)), w + 8);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = x[j] * r * w[j];
+          for (int j = 0; j < 16; ++j) x[j] = x[j] * r * w[j];
+        }
+        if (rl.rot && ra.cos_t != nullptr) rope_rotate<INTER, false>(x, cs, sn);
+        p0 = pack8<BF16>(x);
+        p1 = pack8<BF16>(x + 8);
       }
-      if (rl.rot && ra.cos_t != nullptr) rope_rotate<INTER, false>(x, cs, sn);
-      u0 = pack8<BF16>(x);
-      u1 = pack8<BF16>(x + 8);
-    }
-    if (part == 0) {
-      if (on) {
-        uint8_t* p = static_cast<uint8_t*>(a.q_out) + ((size_t)t * a.q_out_stride + (size_t)h * D) * 2;
-        *reinterpret_cast<uint4*>(p + 2 * rl.c0) = u0;
-        *reinterpret_cast<uint4*>(p + 2 * rl.c1) = u1;
+      if (part == 0) {
+        if (on) {
+          uint8_t* p = static_cast<uint8_t*>(a.q_out) + ((size_t)t_now * a.q_out_stride + (size_t)h * D) * 2;
+          __stcs(reinterpret_cast<uint4*>(p + 2 * rl.c0), p0);
+          __stcs(reinterpret_cast<uint4*>(p + 2 * rl.c1), p1);
+        }
+        continue;
       }
-      continue;
-    }
-    uint8_t* block = static_cast<uint8_t*>(part == 1 ? pg.k_cache : pg.v_cache) +
-                     ((size_t)page * pg.Hk + h) * cache_block_bytes(D, pg.page_size, Q4);
-    if constexpr (!Q4) {
-      if (on) {
-        uint8_t* p = block + (size_t)slot * D * 2;
-        *reinterpret_cast<uint4*>(p + 2 * rl.c0) = u0;
-        *reinterpret_cast<uint4*>(p + 2 * rl.c1) = u1;
-      }
-    } else {
-      // through shared memory: from the rotation's chunks to 16 consecutive features, half a group
-      uint4* row = &s_rows[warp][(lane / G) * (D / 8)];
-      row[rl.c0 / 8] = u0;
-      row[rl.c1 / 8] = u1;
-      __syncwarp();
-      float x[16];
-      unpack8<BF16>(row[2 * l], x);
-      unpack8<BF16>(row[2 * l + 1], x + 8);
-      __syncwarp();
-      uint32_t num[16];
-      const uint32_t pair = quantise16(x, num);
-      const int w = l >> 1, half = l & 1;
-      if (on) {
-        uint8_t* p = block + (size_t)slot * (D / 2);
+      uint8_t* block = static_cast<uint8_t*>(part == 1 ? pg.k_cache : pg.v_cache) +
+                       ((size_t)page * pg.Hk + h) * cache_block_bytes(D, pg.page_size, Q4);
+      if constexpr (!Q4) {
+        if (on) {
+          uint8_t* p = block + (size_t)slot * D * 2;
+          *reinterpret_cast<uint4*>(p + 2 * rl.c0) = p0;
+          *reinterpret_cast<uint4*>(p + 2 * rl.c1) = p1;
+        }
+      } else {
+        // through shared memory: from the rotation's chunks to 16 consecutive features, half a group
+        uint4* row = &s_rows[warp][(lane / G) * (D / 8)];
+        row[rl.c0 / 8] = p0;
+        row[rl.c1 / 8] = p1;
+        __syncwarp();
+        float x[16];
+        unpack8<BF16>(row[2 * l], x);
+        unpack8<BF16>(row[2 * l + 1], x + 8);
+        __syncwarp();
+        uint32_t num[16];  // a number in the low 4 bits of each
+        const uint32_t pair = quantise16(x, num);
+        // and back, from the numbers to the row's bytes in the cache's order, 8 of them a lane
+        const int w = l >> 1, half = l & 1;
         if (part == 1) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int j = 0; j < 2; ++j) {
             uint32_t word = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) word |= num[8 * u + j] << (4 * j);
-            reinterpret_cast<uint32_t*>(p)[(2 * half + u) * W + w] = word;
+            for (int e = 0; e < 8; ++e) word |= (num[8 * j + e] & 15u) << (4 * e);
+            reinterpret_cast<uint32_t*>(row)[(2 * half + j) * W + w] = word;
           }
         } else {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          for (int j = 0; j < 4; ++j) {
             uint32_t word = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) word |= num[4 * u + j] << (4 * j);
-            reinterpret_cast<uint16_t*>(p)[(4 * half + u) * W + w] = (uint16_t)word;
+            for (int e = 0; e < 4; ++e) word |= (num[4 * j + e] & 15u) << (4 * e);
+            reinterpret_cast<uint16_t*>(row)[(4 * half + j) * W + w] = (uint16_t)word;
           }
         }
-        if (half == 0)
-          reinterpret_cast<uint32_t*>(block + (size_t)pg.page_size * (D / 2) + (size_t)slot * (D / 8))[w] = pair;
+        __syncwarp();
+        if (on) {
+          *reinterpret_cast<uint2*>(block + (size_t)slot * (D / 2) + 8 * l) = reinterpret_cast<const uint2*>(row)[l];
+          if (half == 0)
+            reinterpret_cast<uint32_t*>(block + (size_t)pg.page_size * (D / 2) + (size_t)slot * (D / 8))[w] = pair;
+        }
+        __syncwarp();
       }
     }
   }
@@ -208,18 +263,24 @@ static dim3 cache_grid(int T, int groups) {
   return dim3(blocks, max(1, min(groups, 2 * kSmCount / blocks)));
 }
 
+template <int D, bool BF16, bool INTER, bool Q4>
+static cudaError_t launch_append_v(const AppendArgs& a, const RopeArgs& ra, const PagedArgs& pg, cudaStream_t stream) {
+  static std::atomic<unsigned long long> done{0};
+  auto kernel = fa_cache_append_kernel<D, BF16, INTER, Q4>;
+  cudaError_t e = set_smem_once(done, reinterpret_cast<const void*>(kernel), kCacheRing);
+  if (e != cudaSuccess) return e;
+  constexpr int RPW = 512 / D, WARPS = kCacheThreads / 32;
+  const long long units = (long long)a.T * ((a.Hq + RPW - 1) / RPW + 2 * ((pg.Hk + RPW - 1) / RPW));
+  const long long share = (units + kCacheBlocks * kSmCount * WARPS - 1) / (kCacheBlocks * kSmCount * WARPS);
+  const int blocks = (int)((units + share * WARPS - 1) / (share * WARPS));
+  kernel<<<blocks, kCacheThreads, kCacheRing, stream>>>(a, ra, pg, (int)share);
+  return cudaPeekAtLastError();
+}
+
 template <int D, bool BF16>
 static cudaError_t launch_append_t(const AppendArgs& a, const RopeArgs& ra, const PagedArgs& pg, cudaStream_t stream) {
-  constexpr int RPW = 512 / D;
-  const dim3 grid = cache_grid(a.T, (a.Hq + RPW - 1) / RPW + 2 * ((pg.Hk + RPW - 1) / RPW));
-  if (pg.q4) {
-    if (ra.interleaved) fa_cache_append_kernel<D, BF16, true, true><<<grid, kCacheThreads, 0, stream>>>(a, ra, pg);
-    else fa_cache_append_kernel<D, BF16, false, true><<<grid, kCacheThreads, 0, stream>>>(a, ra, pg);
-  } else {
-    if (ra.interleaved) fa_cache_append_kernel<D, BF16, true, false><<<grid, kCacheThreads, 0, stream>>>(a, ra, pg);
-    else fa_cache_append_kernel<D, BF16, false, false><<<grid, kCacheThreads, 0, stream>>>(a, ra, pg);
-  }
-  return cudaPeekAtLastError();
+  if (ra.interleaved) return pg.q4 ? launch_append_v<D, BF16, true, true>(a, ra, pg, stream) : launch_append_v<D, BF16, true, false>(a, ra, pg, stream);
+  return pg.q4 ? launch_append_v<D, BF16, false, true>(a, ra, pg, stream) : launch_append_v<D, BF16, false, false>(a, ra, pg, stream);
 }
 
 cudaError_t launch_cache_append(const AppendArgs& a, const RopeArgs& ra, const PagedArgs& pg, cudaStream_t stream) {
