@@ -37,170 +37,164 @@ __device__ __forceinline__ bool owner_of(const int32_t* cu, int B, int T, int t,
   return true;
 }
 
-// The work is dealt out as units of 512/d rows: for each token the groups of its query heads, of its key heads, of its
-// value heads.  A warp takes a run of units, so few tokens spread over as many warps as there are units, and many tokens
-// keep their lookups and angles for a dozen units.  The rows come ahead through a ring in shared memory; each lane copies
-// the pieces it will read itself, so nothing waits for another thread.
-constexpr int kCacheStages = 8;
-constexpr int kCacheRing = kCacheThreads / 32 * kCacheStages * 2 * 32 * 16;
-constexpr int kCacheBlocks = 3;  // per SM: 168 KB in flight
-
-template <int D, bool BF16, bool INTER, bool Q4>
-__global__ void __launch_bounds__(kCacheThreads, kCacheBlocks) fa_cache_append_kernel(const AppendArgs a, const RopeArgs ra,
-                                                                                      const PagedArgs pg, int share) {
-  constexpr int G = D / 16, RPW = 32 / G, W = D / 32;
-  extern __shared__ __align__(16) uint4 s_ring[];                      // [warps][stages][2 pieces][lanes]
-  __shared__ uint4 s_rows[Q4 ? kCacheThreads / 32 : 1][Q4 ? 64 : 1];  // a warp's rows, 512 values
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G;
-  const int gq = (a.Hq + RPW - 1) / RPW, gk = (pg.Hk + RPW - 1) / RPW, groups = gq + 2 * gk;
-  const long long u0 = ((long long)blockIdx.x * (kCacheThreads / 32) + warp) * share, all = (long long)a.T * groups;
-  if (u0 >= all) return;
-  int left = (int)min((long long)share, all - u0), to_copy = left;
-  int t = (int)(u0 / groups), gi = (int)(u0 - (long long)t * groups);
-  const RopeLane rl = rope_lane<INTER>(l, ra.rot_dim);
-  uint4* mine = s_ring + warp * (kCacheStages * 2 * 32) + lane;
-  int t_next = t, g_next = gi, stage = 0, stage_next = 0;
-  auto issue = [&]() {
-    if (to_copy > 0) {
-      --to_copy;
-      const int part = g_next < gq ? 0 : g_next < gq + gk ? 1 : 2;  // queries, keys, values
-      const int h = (part == 0 ? g_next : part == 1 ? g_next - gq : g_next - gq - gk) * RPW + lane / G;
-      if (h < (part == 0 ? a.Hq : pg.Hk)) {
-        const uint8_t* src = static_cast<const uint8_t*>(part == 0 ? a.q : part == 1 ? a.k : a.v) +
-                             ((size_t)t_next * (part == 0 ? a.q_stride : part == 1 ? a.k_stride : a.v_stride) + (size_t)h * D) * 2;
-        const uint32_t to = smem_u32(mine + stage_next * 64);
-        cp_async16(to, src + 2 * rl.c0);
-        cp_async16(to + 512, src + 2 * rl.c1);
-      }
-      if (++g_next == groups) {
-        g_next = 0;
-        ++t_next;
-      }
-    }
-    stage_next = stage_next + 1 == kCacheStages ? 0 : stage_next + 1;
-    cp_async_commit();
-  };
+// Stores 512/d rows (this lane's two chunks each) of keys or values as 4-bit rows.  `rows`: the warp's 1 KB in shared
+// memory.  From the rotation's chunks to 16 consecutive features a lane (half a group), and from the numbers to the row's
+// bytes in the cache's order, 8 of them a lane.
+template <int D, bool BF16, bool VALUE>
+__device__ __forceinline__ void store_q4(uint4* rows, const RopeLane& rl, int lane, const uint4& p0, const uint4& p1, uint8_t* numbers,
+                                         uint8_t* pairs, bool on) {
+  constexpr int G = D / 16, W = D / 32;
+  const int l = lane % G, w = l >> 1, half = l & 1;
+  uint4* row = rows + lane / G * (D / 8);
+  __syncwarp();  // the rows before are read
+  row[rl.c0 / 8] = p0;
+  row[rl.c1 / 8] = p1;
+  __syncwarp();
+  const uint4 first = row[2 * l], second = row[2 * l + 1];
+  __syncwarp();
+  uint32_t num[16];
+  const uint32_t pair = quantise16<BF16>(first, second, num);
 #pragma unroll
-  for (int s = 0; s < kCacheStages - 1; ++s) issue();
-  float cs[8], sn[8];
-  int page = -1, slot = 0;
-  bool fresh = true;  // the token's lookups are to be made
-#pragma unroll 1
-  for (; left > 0; --left) {
-    if (fresh) {
-      fresh = false;
-      int b, i, n;
-      page = -1;
-      if (owner_of(a.cu_seqlens, pg.B, a.T, t, b, i, n)) {
-        const int len = __ldg(pg.seqlens_k + b);
-        const int at = len - n + i;
-        const int2 pos = rope_positions(ra, t, a.T, at, rl);
-        page = page_of(pg, b, len < n ? -1 : at, slot);
-        if (page >= 0 && !rope_angles(ra, pos, rl, cs, sn)) page = -1;
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t word = nibbles8(num + 8 * j);
+    if constexpr (!VALUE) {
+      reinterpret_cast<uint32_t*>(row)[(2 * half + j) * W + w] = word;
+    } else {
+      reinterpret_cast<uint16_t*>(row)[(4 * half + 2 * j) * W + w] = (uint16_t)word;
+      reinterpret_cast<uint16_t*>(row)[(4 * half + 2 * j + 1) * W + w] = (uint16_t)(word >> 16);
+    }
+  }
+  __syncwarp();
+  if (on) {
+    *reinterpret_cast<uint2*>(numbers + 8 * l) = reinterpret_cast<const uint2*>(row)[l];
+    if (half == 0) *reinterpret_cast<uint32_t*>(pairs + 4 * w) = pair;
+  }
+}
+
+// U: row groups (of 512/d rows) that are loaded together; the first ones are loaded ahead of the token's lookups.  A warp
+// does its token's queries, keys and values, or (gridDim.z = 3) one of the three.
+template <int D, bool BF16, bool INTER, bool Q4, int U>
+__global__ void __launch_bounds__(kCacheThreads, U == 2 ? 3 : 2) fa_cache_append_kernel(const AppendArgs a, const RopeArgs ra, const PagedArgs pg) {
+  constexpr int G = D / 16, RPW = 32 / G;
+  __shared__ uint4 s_rows[Q4 ? kCacheThreads / 32 : 1][Q4 ? 64 : 1];  // a warp's rows, 512 values
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * (kCacheThreads / 32) + warp;
+  if (t >= a.T) return;
+  const RopeLane rl = rope_lane<INTER>(lane % G, ra.rot_dim);
+  const int c0 = 2 * rl.c0, c1 = 2 * rl.c1, h_first = blockIdx.y * (RPW * U) + lane / G;
+  const uint8_t* src = nullptr;
+  int H = 0;
+  uint4 v0[U], v1[U];
+  auto begin = [&](const void* x, long long stride, int heads) {
+    src = static_cast<const uint8_t*>(x) + (t * stride + (long long)h_first * D) * 2;
+    H = heads;
+  };
+  auto load = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      v0[u] = v1[u] = make_uint4(0, 0, 0, 0);
+      if (h + u * RPW < H) {
+        v0[u] = __ldcs(reinterpret_cast<const uint4*>(src + u * RPW * D * 2 + c0));
+        v1[u] = __ldcs(reinterpret_cast<const uint4*>(src + u * RPW * D * 2 + c1));
       }
     }
-    const int part = gi < gq ? 0 : gi < gq + gk ? 1 : 2, t_now = t;
-    const int h = (part == 0 ? gi : part == 1 ? gi - gq : gi - gq - gk) * RPW + lane / G;
-    const bool on = h < (part == 0 ? a.Hq : pg.Hk);
-    if (++gi == groups) {
-      gi = 0;
-      ++t;
-      fresh = true;
+    src += (size_t)gridDim.y * (RPW * U * D * 2);
+  };
+  const int part0 = gridDim.z == 1 ? (a.Hq > 0 ? 0 : 1) : blockIdx.z, parts = gridDim.z == 1 ? 3 : part0 + 1;
+  if (part0 == 0) begin(a.q, a.q_stride, a.Hq);
+  else if (part0 == 1) begin(a.k, a.k_stride, pg.Hk);
+  else begin(a.v, a.v_stride, pg.Hk);
+  load(h_first);
+
+  int b, i, n;
+  if (!owner_of(a.cu_seqlens, pg.B, a.T, t, b, i, n)) return;
+  const int len = __ldg(pg.seqlens_k + b);
+  const int at = len - n + i;
+  const int2 pos = rope_positions(ra, t, a.T, at, rl);
+  int slot;
+  const int page = page_of(pg, b, len < n ? -1 : at, slot);
+  if (page < 0) return;
+  float cs[8], sn[8];
+  if (!rope_angles(ra, pos, rl, cs, sn)) return;
+
+  // queries and keys
+#pragma unroll 1
+  for (int part = part0; part < min(parts, 2); ++part) {
+    const void* wp = part == 0 ? a.wq : a.wk;
+    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+    if (wp != nullptr) {
+      w0 = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + c0));
+      w1 = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + c1));
     }
-    cp_async_wait<kCacheStages - 2>();
-    const uint4* from = mine + stage * 64;
-    stage = stage + 1 == kCacheStages ? 0 : stage + 1;
-    uint4 p0 = make_uint4(0, 0, 0, 0), p1 = p0;
-    if (on) {
-      p0 = from[0];
-      p1 = from[32];
-    }
-    issue();  // into the place that the last turn read
-    if (page < 0) continue;  // no sequence's token, or one that cannot be placed
-    {
-      const void* wp = part == 0 ? a.wq : part == 1 ? a.wk : nullptr;
-      if (part < 2 && (wp != nullptr || ra.cos_t != nullptr)) {
+    const size_t block = cache_block_bytes(D, pg.page_size, Q4);
+    uint8_t* dst = part == 0 ? static_cast<uint8_t*>(a.q_out) + (t * a.q_out_stride + (long long)h_first * D) * 2
+                             : static_cast<uint8_t*>(pg.k_cache) + ((size_t)page * pg.Hk + h_first) * block + (size_t)slot * (Q4 ? D / 2 : D * 2);
+    const size_t next = part == 0 ? (size_t)RPW * D * 2 : RPW * block;
+    const bool packed = Q4 && part == 1;
+#pragma unroll 1
+    for (int h = h_first; h - lane / G < H; h += gridDim.y * (RPW * U)) {
+      if (h != h_first) load(h);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
         float x[16];
-        unpack8<BF16>(p0, x);
-        unpack8<BF16>(p1, x + 8);
+        unpack8<BF16>(v0[u], x);
+        unpack8<BF16>(v1[u], x + 8);
         if (wp != nullptr) {
           const float r = row_rms_inv<D>(x, a.eps);
           float w[16];
-          const uint8_t* p = static_cast<const uint8_t*>(wp);
-          unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(p + 2 * rl.c0)), w);
-          unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(p + 2 * rl.c1)), w + 8);
+          unpack8<BF16>(w0, w);
+          unpack8<BF16>(w1, w + 8);
 #pragma unroll
           for (int j = 0; j < 16; ++j) x[j] = x[j] * r * w[j];
         }
         if (rl.rot && ra.cos_t != nullptr) rope_rotate<INTER, false>(x, cs, sn);
-        p0 = pack8<BF16>(x);
-        p1 = pack8<BF16>(x + 8);
+        const uint4 p0 = pack8<BF16>(x), p1 = pack8<BF16>(x + 8);
+        const bool on = h + u * RPW < H;
+        if (packed) {
+          if constexpr (Q4)
+            store_q4<D, BF16, false>(s_rows[warp], rl, lane, p0, p1, dst + u * next,
+                                     dst + u * next + (size_t)(pg.page_size - slot) * (D / 2) + (size_t)slot * (D / 8), on);
+        } else if (on) {
+          __stcs(reinterpret_cast<uint4*>(dst + u * next + c0), p0);
+          __stcs(reinterpret_cast<uint4*>(dst + u * next + c1), p1);
+        }
       }
-      if (part == 0) {
-        if (on) {
-          uint8_t* p = static_cast<uint8_t*>(a.q_out) + ((size_t)t_now * a.q_out_stride + (size_t)h * D) * 2;
-          __stcs(reinterpret_cast<uint4*>(p + 2 * rl.c0), p0);
-          __stcs(reinterpret_cast<uint4*>(p + 2 * rl.c1), p1);
-        }
-        continue;
-      }
-      uint8_t* block = static_cast<uint8_t*>(part == 1 ? pg.k_cache : pg.v_cache) +
-                       ((size_t)page * pg.Hk + h) * cache_block_bytes(D, pg.page_size, Q4);
-      if constexpr (!Q4) {
-        if (on) {
-          uint8_t* p = block + (size_t)slot * D * 2;
-          *reinterpret_cast<uint4*>(p + 2 * rl.c0) = p0;
-          *reinterpret_cast<uint4*>(p + 2 * rl.c1) = p1;
-        }
-      } else {
-        // through shared memory: from the rotation's chunks to 16 consecutive features, half a group
-        uint4* row = &s_rows[warp][(lane / G) * (D / 8)];
-        row[rl.c0 / 8] = p0;
-        row[rl.c1 / 8] = p1;
-        __syncwarp();
-        float x[16];
-        unpack8<BF16>(row[2 * l], x);
-        unpack8<BF16>(row[2 * l + 1], x + 8);
-        __syncwarp();
-        uint32_t num[16];  // a number in the low 4 bits of each
-        const uint32_t pair = quantise16(x, num);
-        // and back, from the numbers to the row's bytes in the cache's order, 8 of them a lane
-        const int w = l >> 1, half = l & 1;
-        if (part == 1) {
+      dst += gridDim.y * U * next;
+    }
+    if (part + 1 < parts) {
+      if (part == 0) begin(a.k, a.k_stride, pg.Hk);
+      else begin(a.v, a.v_stride, pg.Hk);
+      load(h_first);
+    }
+  }
+  if (parts < 3) return;
+  // values
+  const size_t next = RPW * cache_block_bytes(D, pg.page_size, Q4);
+  uint8_t* dst = static_cast<uint8_t*>(pg.v_cache) + ((size_t)page * pg.Hk + h_first) * (next / RPW) + (size_t)slot * (Q4 ? D / 2 : D * 2);
+#pragma unroll 1
+  for (int h = h_first; h - lane / G < H; h += gridDim.y * (RPW * U)) {
+    if (h != h_first) load(h);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t word = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) word |= (num[8 * j + e] & 15u) << (4 * e);
-            reinterpret_cast<uint32_t*>(row)[(2 * half + j) * W + w] = word;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t word = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) word |= (num[4 * j + e] & 15u) << (4 * e);
-            reinterpret_cast<uint16_t*>(row)[(4 * half + j) * W + w] = (uint16_t)word;
-          }
-        }
-        __syncwarp();
-        if (on) {
-          *reinterpret_cast<uint2*>(block + (size_t)slot * (D / 2) + 8 * l) = reinterpret_cast<const uint2*>(row)[l];
-          if (half == 0)
-            reinterpret_cast<uint32_t*>(block + (size_t)pg.page_size * (D / 2) + (size_t)slot * (D / 8))[w] = pair;
-        }
-        __syncwarp();
+    for (int u = 0; u < U; ++u) {
+      const bool on = h + u * RPW < H;
+      if constexpr (Q4) {
+        store_q4<D, BF16, true>(s_rows[warp], rl, lane, v0[u], v1[u], dst + u * next,
+                                dst + u * next + (size_t)(pg.page_size - slot) * (D / 2) + (size_t)slot * (D / 8), on);
+      } else if (on) {
+        __stcs(reinterpret_cast<uint4*>(dst + u * next + c0), v0[u]);
+        __stcs(reinterpret_cast<uint4*>(dst + u * next + c1), v1[u]);
       }
     }
+    dst += gridDim.y * U * next;
   }
 }
 
-// 16 consecutive values (half a group) from their 4-bit numbers.
-__device__ __forceinline__ void dequantise16(const uint32_t (&n)[16], uint32_t pair, float (&x)[16]) {
-  const float sc = __half2float(__ushort_as_half((unsigned short)(pair & 0xffffu)));
-  const float mn = __half2float(__ushort_as_half((unsigned short)(pair >> 16)));
+// N consecutive numbers from the low bits of `word` on, as values.
+template <int N>
+__device__ __forceinline__ void dequantise(uint32_t word, uint32_t pair, float* x) {
+  const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&pair));
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = fmaf((float)n[i], sc, mn);
+  for (int i = 0; i < N; ++i) x[i] = fmaf((float)((word >> (4 * i)) & 15u), p.x, p.y);
 }
 
 template <int D, bool BF16, bool Q4>
@@ -226,33 +220,38 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_gather_kernel(const Ga
     uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(isv ? a.v : a.k) + ((size_t)t * pg.Hk + h) * D * 2);
     if constexpr (!Q4) {
       const uint4* p = reinterpret_cast<const uint4*>(block + (size_t)slot * D * 2);
-      const uint4 u0 = __ldg(p + l), u1 = __ldg(p + G + l);
-      out[l] = u0;
-      out[G + l] = u1;
+      const uint4 u0 = __ldcs(p + l), u1 = __ldcs(p + G + l);
+      __stcs(out + l, u0);
+      __stcs(out + G + l, u1);
     } else {
-      const uint8_t* p = block + (size_t)slot * (D / 2);
-      const int w = l >> 1, half = l & 1;
-      const uint32_t pair = __ldg(reinterpret_cast<const uint32_t*>(block + (size_t)pg.page_size * (D / 2) + (size_t)slot * (D / 8)) + w);
-      uint32_t num[16];
+      // 8 bytes of the row a lane: of a key two words, 8 features each of two groups; of a value four half words, 4 features each
+      const uint2 word = __ldcs(reinterpret_cast<const uint2*>(block + (size_t)slot * (D / 2)) + l);
+      const uint8_t* pairs = block + (size_t)pg.page_size * (D / 2) + (size_t)slot * (D / 8);
       if (!isv) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t word = __ldg(reinterpret_cast<const uint32_t*>(p) + (2 * half + u) * W + w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) num[8 * u + j] = (word >> (4 * j)) & 15u;
-        }
+        const int t4 = 2 * l / W, w = 2 * l % W;
+        const uint2 pair = __ldg(reinterpret_cast<const uint2*>(pairs + 4 * w));
+        float x[8], y[8];
+        dequantise<8>(word.x, pair.x, x);
+        dequantise<8>(word.y, pair.y, y);
+        __stcs(out + 4 * w + t4, pack8<BF16>(x));
+        __stcs(out + 4 * w + 4 + t4, pack8<BF16>(y));
       } else {
+        uint32_t pair[W];
+        if constexpr (W == 4) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(pairs));
+          pair[0] = v.x; pair[1] = v.y; pair[2] = v.z; pair[3] = v.w;
+        } else {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(pairs));
+          pair[0] = v.x; pair[1] = v.y;
+        }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t word = __ldg(reinterpret_cast<const uint16_t*>(p) + (4 * half + u) * W + w);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) num[4 * u + j] = (word >> (4 * j)) & 15u;
+        for (int j = 0; j < 4; ++j) {
+          const int g = 4 * l / W + j / W, w = j % W;
+          float x[4];
+          dequantise<4>((j & 2 ? word.y : word.x) >> (16 * (j & 1)), pair[w], x);
+          __stcs(reinterpret_cast<uint2*>(out) + 8 * w + g, make_uint2(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3])));
         }
       }
-      float x[16];
-      dequantise16(num, pair, x);
-      out[2 * l] = pack8<BF16>(x);
-      out[2 * l + 1] = pack8<BF16>(x + 8);
     }
   }
 }
@@ -263,24 +262,23 @@ static dim3 cache_grid(int T, int groups) {
   return dim3(blocks, max(1, min(groups, 2 * kSmCount / blocks)));
 }
 
-template <int D, bool BF16, bool INTER, bool Q4>
-static cudaError_t launch_append_v(const AppendArgs& a, const RopeArgs& ra, const PagedArgs& pg, cudaStream_t stream) {
-  static std::atomic<unsigned long long> done{0};
-  auto kernel = fa_cache_append_kernel<D, BF16, INTER, Q4>;
-  cudaError_t e = set_smem_once(done, reinterpret_cast<const void*>(kernel), kCacheRing);
-  if (e != cudaSuccess) return e;
-  constexpr int RPW = 512 / D, WARPS = kCacheThreads / 32;
-  const long long units = (long long)a.T * ((a.Hq + RPW - 1) / RPW + 2 * ((pg.Hk + RPW - 1) / RPW));
-  const long long share = (units + kCacheBlocks * kSmCount * WARPS - 1) / (kCacheBlocks * kSmCount * WARPS);
-  const int blocks = (int)((units + share * WARPS - 1) / (share * WARPS));
-  kernel<<<blocks, kCacheThreads, kCacheRing, stream>>>(a, ra, pg, (int)share);
+template <int D, bool BF16, bool Q4, int U>
+static cudaError_t launch_append_u(const AppendArgs& a, const RopeArgs& ra, const PagedArgs& pg, cudaStream_t stream) {
+  constexpr int ROWS = 512 / D * U;
+  dim3 grid = cache_grid(a.T, (max(a.Hq, pg.Hk) + ROWS - 1) / ROWS);
+  if (U == 1) grid.z = 3;
+  if (ra.interleaved) fa_cache_append_kernel<D, BF16, true, Q4, U><<<grid, kCacheThreads, 0, stream>>>(a, ra, pg);
+  else fa_cache_append_kernel<D, BF16, false, Q4, U><<<grid, kCacheThreads, 0, stream>>>(a, ra, pg);
   return cudaPeekAtLastError();
 }
 
+// Two row groups together where the tokens fill the GPU; else one, with the heads, and queries, keys and values, spread
+// over blocks too.
 template <int D, bool BF16>
 static cudaError_t launch_append_t(const AppendArgs& a, const RopeArgs& ra, const PagedArgs& pg, cudaStream_t stream) {
-  if (ra.interleaved) return pg.q4 ? launch_append_v<D, BF16, true, true>(a, ra, pg, stream) : launch_append_v<D, BF16, true, false>(a, ra, pg, stream);
-  return pg.q4 ? launch_append_v<D, BF16, false, true>(a, ra, pg, stream) : launch_append_v<D, BF16, false, false>(a, ra, pg, stream);
+  const bool many = a.T >= 2 * kSmCount * (kCacheThreads / 32);
+  if (pg.q4) return many ? launch_append_u<D, BF16, true, 2>(a, ra, pg, stream) : launch_append_u<D, BF16, true, 1>(a, ra, pg, stream);
+  return many ? launch_append_u<D, BF16, false, 2>(a, ra, pg, stream) : launch_append_u<D, BF16, false, 1>(a, ra, pg, stream);
 }
 
 cudaError_t launch_cache_append(const AppendArgs& a, const RopeArgs& ra, const PagedArgs& pg, cudaStream_t stream) {

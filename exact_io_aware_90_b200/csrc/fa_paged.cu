@@ -383,7 +383,7 @@ struct Rows16 {
     bool rise = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-      rise = rise || fmaxf(s[nt][0], s[nt][2]) > rise_at[nt][0] || fmaxf(s[nt][1], s[nt][3]) > rise_at[nt][1];
+      rise |= (fmaxf(s[nt][0], s[nt][2]) > rise_at[nt][0]) | (fmaxf(s[nt][1], s[nt][3]) > rise_at[nt][1]);
     if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -699,7 +699,7 @@ struct Rows4 {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        rise = rise || top_of(s, nt, u) > rise_at[nt][u];
+        rise |= top_of(s, nt, u) > rise_at[nt][u];
     if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
