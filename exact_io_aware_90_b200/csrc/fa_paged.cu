@@ -37,12 +37,14 @@
 //   * Each group of 32 features has its own fp32 accumulator, which the key's scale multiplies; the minima times the
 //     sums of q over the groups are one small product (the sums as two fp16 parts).
 //   * P is rounded to fp16 and transposed once; for each group it is then multiplied by the values' scales of its keys.
+//     That rounds a second time, which bf16 outputs do not show; for fp16 outputs what the second rounding takes away is
+//     a product of its own (both roundings together left 1.8 times the output's own error, one leaves 1.4).
 //   * Σ_j p_j·min_j and Σ_j p_j·scale_j are one small product more.  It takes the same rounded P, so what rounding
 //     leaves is relative to the value, n·scale + min, and not to the larger min.
 //   * The values enter as n − 8.  Without the shift the products would add up to a mean of 2 standard deviations per
 //     key that the minimum takes away again: over 131071 keys the tensor cores' truncating sums left 8e-4 of the
 //     output.  For one row tile −8·ΣP is a product of its own (no instruction per number); two row tiles share a
-//     subtraction per number.
+//     subtraction per number, and so do fp16 outputs.
 //   * The reference is 2^7 below the maximum (less where scales pass 1), so that fp16's range serves P from 2^15 down.
 #include <type_traits>
 
@@ -173,6 +175,13 @@ __device__ __forceinline__ GranuleScan scan_granules(const PagedParams& p) {
 // Granules that each worker takes.
 __device__ __forceinline__ long long granule_share(const PagedParams& p, long long total) {
   return max(1LL, quotient(total + p.workers - 1, p.workers));
+}
+
+// What rounding took from the products: a·b − ab, exact.
+__device__ __forceinline__ uint32_t rest_f16x2(uint32_t a, uint32_t b, uint32_t ab) {
+  uint32_t d;
+  asm("{\n\t.reg .b32 t;\n\tneg.f16x2 t, %3;\n\tfma.rn.f16x2 %0, %1, %2, t;\n\t}" : "=r"(d) : "r"(a), "r"(b), "r"(ab));
+  return d;
 }
 
 // What a part with maximum m weighs beside the maximum of all, M.  Parts without a key (m = -inf) hold zeros, or
@@ -501,7 +510,8 @@ struct Rows16 {
 template <int D, bool BF16, int NT>
 struct Rows4 {
   static constexpr int W = D / 32, KS = D / 16, ROW = D / 2, PAIR = D / 8;
-  static constexpr bool kCentre = NT == 1;  // −8·ΣP as a product
+  static constexpr bool kRest = !BF16;              // P·scale in two parts
+  static constexpr bool kCentre = NT == 1 && !kRest;  // −8·ΣP as a product
   static constexpr int NS = 2;  // sub-tiles in flight together
   static constexpr float kDepth = 7.f;      // the reference is 2^7 under the maximum
   uint32_t qb[NT][KS][2], qs[NT];
@@ -809,6 +819,11 @@ struct Rows4 {
             if constexpr (kCentre)  // −8·2^-24 for the even numbers, −8·2^-20 for the odd ones
               mma_16816<false>(o[nt][2 * j + u], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
             mma_16816<false>(o[nt][2 * j + u], a[u][0], a[u][1], a[u][2], a[u][3], b0, b1);
+          }
+          if constexpr (kRest) {
+            const uint32_t r0 = rest_f16x2(bh[nt][0], s01, b0), r1 = rest_f16x2(bh[nt][1], s89, b1);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) mma_16816<false>(o[nt][2 * j + u], a[u][0], a[u][1], a[u][2], a[u][3], r0, r1);
           }
         }
       }
