@@ -1,8 +1,8 @@
-"""Builds libfa_b200.so in-tree with nvcc for sm_100a.
+"""Builds libfa_b200.so in-tree with nvcc for sm_100a, and the torch binding of the wrappers (_binding.so) with g++.
 
 Usage: python exact_io_aware_90_b200/build.py [--verbose-ptxas]   (by path: importing the package would load the
 existing library first)
-The library lands next to this file; the Python binding loads it from there.
+Both land next to this file; the Python package loads them from there.
 """
 from __future__ import annotations
 
@@ -16,6 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB_NAME = "libfa_b200.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+BINDING_PATH = os.path.join(HERE, "_binding.so")
 SOURCES = ["libfa_b200.cu"]
 DEPS = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu", "fa_merge.cu", "fa_noalloc.cu", "fa_rope.cu",
         "fa_cache.cu", "fa_paged.cu", "fa_paged_api.cu"]
@@ -29,16 +30,46 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found: set NVCC or put the CUDA toolkit on PATH")
 
 
-def needs_rebuild() -> bool:
-    if not os.path.exists(LIB_PATH):
+def _older(path: str, deps) -> bool:
+    if not os.path.exists(path):
         return True
-    t = os.path.getmtime(LIB_PATH)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + DEPS + HEADERS] + [__file__]
+    t = os.path.getmtime(path)
     return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
+
+
+def needs_rebuild() -> bool:
+    return _older(LIB_PATH, [os.path.join(CSRC, f) for f in SOURCES + DEPS + HEADERS] + [__file__])
+
+
+def build_binding(force: bool = False) -> str:
+    """The torch binding: linked against this interpreter's torch and, by a path relative to itself, the library."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and not _older(BINDING_PATH, [src, os.path.join(ROOT, "include", "fa.h"), __file__]):
+        return BINDING_PATH
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include")
+    # the system compiler, not $CXX: a toolchain that links libstdc++ in statically breaks against torch's shared one
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda,
+           "-I", sysconfig.get_paths()["include"], src, "-o", BINDING_PATH + ".tmp",
+           "-L", libs, "-L", HERE, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lfa_b200",
+           "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("g++ failed building " + os.path.basename(BINDING_PATH))
+    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+    return BINDING_PATH
 
 
 def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     if not force and not needs_rebuild():
+        build_binding()
         return LIB_PATH
     cmd = [
         nvcc_path(),
@@ -58,6 +89,7 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     if verbose_ptxas:
         sys.stderr.write(res.stderr)
     os.replace(LIB_PATH + ".tmp", LIB_PATH)
+    build_binding(force)
     return LIB_PATH
 
 
