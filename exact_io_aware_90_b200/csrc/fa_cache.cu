@@ -189,15 +189,22 @@ __global__ void __launch_bounds__(kCacheThreads, U == 2 ? 3 : 2) fa_cache_append
   }
 }
 
-// N consecutive numbers from the low bits of `word` on, as values.
-template <int N>
-__device__ __forceinline__ void dequantise(uint32_t word, uint32_t pair, float* x) {
-  const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&pair));
+// The eight numbers of a word as values x[0..7]: pairs (n, n + 4) under the exponent of 1024, the numbers exact in fp16.
+__device__ __forceinline__ void dequantise8(uint32_t word, float2 p0, float2 p1, float* x) {
+  const __half2 base = __float2half2_rn(1024.f);
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = fmaf((float)((word >> (4 * i)) & 15u), p.x, p.y);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t m = ((word >> (4 * i)) & 0x000f000fu) | 0x64006400u;
+    const float2 n = __half22float2(__hsub2(*reinterpret_cast<const __half2*>(&m), base));
+    x[i] = fmaf(n.x, p0.x, p0.y);
+    x[i + 4] = fmaf(n.y, p1.x, p1.y);
+  }
 }
 
-template <int D, bool BF16, bool Q4>
+__device__ __forceinline__ float2 pair_of(uint32_t pair) { return __half22float2(*reinterpret_cast<const __half2*>(&pair)); }
+
+// U groups of 512/d heads are loaded together, keys and values: a 4-bit row has few bytes, so many have to be in flight.
+template <int D, bool BF16, bool Q4, int U>
 __global__ void __launch_bounds__(kCacheThreads) fa_cache_gather_kernel(const GatherArgs a, const PagedArgs pg) {
   constexpr int G = D / 16, RPW = 32 / G, W = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G;
@@ -209,49 +216,79 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_gather_kernel(const Ga
   int slot;
   const int page = page_of(pg, b, start < 0 || start > 0x7fffffff - i ? -1 : start + i, slot);
   if (page < 0) return;
-  const int gk = (pg.Hk + RPW - 1) / RPW;
+  const size_t block = cache_block_bytes(D, pg.page_size, Q4);
+  const size_t first = ((size_t)page * pg.Hk + lane / G) * block, row = (size_t)slot * (Q4 ? D / 2 : D * 2);
+  const uint8_t* kb = static_cast<const uint8_t*>(pg.k_cache) + first;
+  const uint8_t* vb = static_cast<const uint8_t*>(pg.v_cache) + first;
+  const size_t out0 = ((size_t)t * pg.Hk + lane / G) * D * 2;
+  uint8_t* ko = static_cast<uint8_t*>(a.k) + out0;
+  uint8_t* vo = static_cast<uint8_t*>(a.v) + out0;
 #pragma unroll 1
-  for (int gi = blockIdx.y; gi < 2 * gk; gi += gridDim.y) {
-    const bool isv = gi >= gk;
-    const int h = (isv ? gi - gk : gi) * RPW + lane / G;
-    if (h >= pg.Hk) continue;
-    const uint8_t* block = static_cast<const uint8_t*>(isv ? pg.v_cache : pg.k_cache) +
-                           ((size_t)page * pg.Hk + h) * cache_block_bytes(D, pg.page_size, Q4);
-    uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(isv ? a.v : a.k) + ((size_t)t * pg.Hk + h) * D * 2);
+  for (int h = blockIdx.y * (RPW * U) + lane / G; h - lane / G < pg.Hk; h += gridDim.y * (RPW * U)) {
+    const int off = h - lane / G;
     if constexpr (!Q4) {
-      const uint4* p = reinterpret_cast<const uint4*>(block + (size_t)slot * D * 2);
-      const uint4 u0 = __ldcs(p + l), u1 = __ldcs(p + G + l);
-      __stcs(out + l, u0);
-      __stcs(out + G + l, u1);
-    } else {
-      // 8 bytes of the row a lane: of a key two words, 8 features each of two groups; of a value four half words, 4 features each
-      const uint2 word = __ldcs(reinterpret_cast<const uint2*>(block + (size_t)slot * (D / 2)) + l);
-      const uint8_t* pairs = block + (size_t)pg.page_size * (D / 2) + (size_t)slot * (D / 8);
-      if (!isv) {
-        const int t4 = 2 * l / W, w = 2 * l % W;
-        const uint2 pair = __ldg(reinterpret_cast<const uint2*>(pairs + 4 * w));
-        float x[8], y[8];
-        dequantise<8>(word.x, pair.x, x);
-        dequantise<8>(word.y, pair.y, y);
-        __stcs(out + 4 * w + t4, pack8<BF16>(x));
-        __stcs(out + 4 * w + 4 + t4, pack8<BF16>(y));
-      } else {
-        uint32_t pair[W];
-        if constexpr (W == 4) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(pairs));
-          pair[0] = v.x; pair[1] = v.y; pair[2] = v.z; pair[3] = v.w;
-        } else {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(pairs));
-          pair[0] = v.x; pair[1] = v.y;
+      uint4 x[U][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h + u * RPW < pg.Hk) {
+          const uint4* pk = reinterpret_cast<const uint4*>(kb + (off + u * RPW) * block + row);
+          const uint4* pv = reinterpret_cast<const uint4*>(vb + (off + u * RPW) * block + row);
+          x[u][0] = __ldcs(pk + l);
+          x[u][1] = __ldcs(pk + G + l);
+          x[u][2] = __ldcs(pv + l);
+          x[u][3] = __ldcs(pv + G + l);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int g = 4 * l / W + j / W, w = j % W;
-          float x[4];
-          dequantise<4>((j & 2 ? word.y : word.x) >> (16 * (j & 1)), pair[w], x);
-          __stcs(reinterpret_cast<uint2*>(out) + 8 * w + g, make_uint2(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3])));
+      for (int u = 0; u < U; ++u)
+        if (h + u * RPW < pg.Hk) {
+          uint4* qk = reinterpret_cast<uint4*>(ko + (size_t)(off + u * RPW) * D * 2);
+          uint4* qv = reinterpret_cast<uint4*>(vo + (size_t)(off + u * RPW) * D * 2);
+          __stcs(qk + l, x[u][0]);
+          __stcs(qk + G + l, x[u][1]);
+          __stcs(qv + l, x[u][2]);
+          __stcs(qv + G + l, x[u][3]);
         }
-      }
+    } else {
+      // 8 bytes of a row a lane: of a key two words, 8 features each of two groups; of a value four half words, 4 each
+      const int t4 = 2 * l / W, w2 = 2 * l % W;
+      const size_t pairs = (size_t)pg.page_size * (D / 2) + (size_t)slot * (D / 8);
+      uint2 kn[U], vn[U], kp[U];
+      uint32_t vp[U][W];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h + u * RPW < pg.Hk) {
+          const uint8_t* pk = kb + (off + u * RPW) * block;
+          const uint8_t* pv = vb + (off + u * RPW) * block;
+          kn[u] = __ldcs(reinterpret_cast<const uint2*>(pk + row) + l);
+          vn[u] = __ldcs(reinterpret_cast<const uint2*>(pv + row) + l);
+          kp[u] = __ldg(reinterpret_cast<const uint2*>(pk + pairs + 4 * w2));
+          if constexpr (W == 4) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(pv + pairs));
+            vp[u][0] = v.x; vp[u][1] = v.y; vp[u][2] = v.z; vp[u][3] = v.w;
+          } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(pv + pairs));
+            vp[u][0] = v.x; vp[u][1] = v.y;
+          }
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h + u * RPW < pg.Hk) {
+          uint4* qk = reinterpret_cast<uint4*>(ko + (size_t)(off + u * RPW) * D * 2);
+          uint2* qv = reinterpret_cast<uint2*>(vo + (size_t)(off + u * RPW) * D * 2);
+          const float2 p0 = pair_of(kp[u].x), p1 = pair_of(kp[u].y);
+          float x[8];
+          dequantise8(kn[u].x, p0, p0, x);
+          __stcs(qk + 4 * w2 + t4, pack8<BF16>(x));
+          dequantise8(kn[u].y, p1, p1, x);
+          __stcs(qk + 4 * w2 + 4 + t4, pack8<BF16>(x));
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {  // half words 4l + j and 4l + j + 1, of groups w and w + 1
+            const int g = 4 * l / W + j / W, w = j % W;
+            dequantise8(j ? vn[u].y : vn[u].x, pair_of(vp[u][w]), pair_of(vp[u][w + 1]), x);
+            __stcs(qv + 8 * w + g, make_uint2(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3])));
+            __stcs(qv + 8 * (w + 1) + g, make_uint2(pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7])));
+          }
+        }
     }
   }
 }
@@ -289,9 +326,14 @@ cudaError_t launch_cache_append(const AppendArgs& a, const RopeArgs& ra, const P
 template <int D, bool BF16>
 static cudaError_t launch_gather_t(const GatherArgs& a, const PagedArgs& pg, cudaStream_t stream) {
   constexpr int RPW = 512 / D;
-  const dim3 grid = cache_grid(a.T, 2 * ((pg.Hk + RPW - 1) / RPW));
-  if (pg.q4) fa_cache_gather_kernel<D, BF16, true><<<grid, kCacheThreads, 0, stream>>>(a, pg);
-  else fa_cache_gather_kernel<D, BF16, false><<<grid, kCacheThreads, 0, stream>>>(a, pg);
+  const bool many = a.T >= 2 * kSmCount * (kCacheThreads / 32) && pg.Hk > RPW;
+  const dim3 grid = cache_grid(a.T, (pg.Hk + RPW - 1) / RPW);
+  if (pg.q4) {
+    if (many) fa_cache_gather_kernel<D, BF16, true, 2><<<grid, kCacheThreads, 0, stream>>>(a, pg);
+    else fa_cache_gather_kernel<D, BF16, true, 1><<<grid, kCacheThreads, 0, stream>>>(a, pg);
+  } else {
+    fa_cache_gather_kernel<D, BF16, false, 1><<<grid, kCacheThreads, 0, stream>>>(a, pg);
+  }
   return cudaPeekAtLastError();
 }
 
