@@ -506,9 +506,13 @@ PyObject* decode_paged(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int bound = as_int(Nk, "max_seqlen_k");
     const Place at_(a, dev);
     const Tensor out = oo != nullptr ? *oo : at_.empty(q.sizes(), dtype), lse = ol != nullptr ? *ol : at_.empty(rows, at::kFloat);
-    const Tensor ws = ow != nullptr ? *ow : at_.empty({static_cast<int64_t>(fa_decode_paged_workspace_bytes(c.B, Nq, H, c.heads, bound, c.d) + 256)}, at::kByte);
+    const size_t need = ow != nullptr ? 0 : fa_decode_paged_workspace_bytes(c.B, Nq, H, c.heads, bound, c.d);
+    Tensor ws;  // small calls need none
+    if (ow != nullptr) ws = *ow;
+    else if (need > 0) ws = at_.empty({static_cast<int64_t>(need)}, at::kByte);
     check(fa_decode_paged(q.data_ptr(), c.k, c.v, out.data_ptr(), lse.data_ptr<float>(), c.table, lens, c.B, Nq, H, c.heads, bound, c.d,
-                          static_cast<float>(scale), c.page_size, c.pages, c.most, code, c.format, ws.data_ptr(), ws.nbytes(), at_.stream),
+                          static_cast<float>(scale), c.page_size, c.pages, c.most, code, c.format, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0,
+                          at_.stream),
           "fa_decode_paged");
     return wrap_tuple(&out, &lse);
   });

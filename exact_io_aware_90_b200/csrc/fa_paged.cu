@@ -6,6 +6,8 @@
 //                          run is finished there; of others each block leaves its partial (m, ℓ, Õ = Σ_j 2^(s_j − m) v_j),
 //                          s = scale·log2(e)·q·k (base 2)
 //   fa_paged_merge_kernel  joins the parts of a row: m = max m_c, ℓ = Σ ℓ_c·2^(m_c − m), Õ the same way
+//   fa_paged_cluster_kernel  small calls: a cluster of blocks per unit, joined through distributed shared memory, so that
+//                          one launch does the call
 //
 // The query rows of a key head are its H/Hk query heads times the Nq new tokens; 8 or 16 of them share one
 // pass over the keys, so a key is read once for the whole group.  The call is a stream over the cache, and
@@ -46,6 +48,8 @@
 //     output.  For one row tile −8·ΣP is a product of its own (no instruction per number); two row tiles share a
 //     subtraction per number, and so do fp16 outputs.
 //   * The reference is 2^7 below the maximum (less where scales pass 1), so that fp16's range serves P from 2^15 down.
+#include <cooperative_groups.h>
+
 #include <type_traits>
 
 #include "paged.cuh"
@@ -844,22 +848,141 @@ struct Rows4 {
   }
 };
 
-template <int D, bool BF16, bool Q4, int NT>
-__global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlocks)) fa_paged_split_kernel(const PagedParams p) {
+// One block's work on granules first .. last − 1 of a unit (first == last: none): every row's maximum, sum and output over
+// those keys, `emit`ted by the row's warp, d/32 features a lane.  `smem`: Cfg::kSmem bytes; the caller synchronises before
+// it calls again.
+template <int D, bool BF16, bool Q4, int NT, typename Emit>
+__device__ __forceinline__ void run_piece(const PagedParams& p, uint8_t* smem, int b, int hk, int r0, int L, int first, int last, Emit&& emit) {
   using Cfg = PagedConfig<D, Q4, NT>;
   using Rows = std::conditional_t<Q4, Rows4<D, BF16, NT>, Rows16<D, BF16, NT>>;
   constexpr int W = D / 32, ROWS = 8 * NT, S = Cfg::kStages, GK = Cfg::kGranule, T = Cfg::kTile;
-  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kPagedWarps][ROWS], s_l[kPagedWarps][ROWS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_u32(smem) + warp * S * Cfg::kTileBytes;
   float* s_o = reinterpret_cast<float*>(smem);
   const int ps = p.pg.page_size;
-  const int units = p.pg.Hk * p.tiles;  // of one sequence
   const bool paired = Q4 && ps % 32 != 0;  // a tile's two halves may lie in two pages
+  const int step_pages = GK / ps, step_slots = GK - step_pages * ps;
+
+      // ---- the warp's tiles, keys GK·i + T·warp on; page lookups run one tile ahead of the copies
+      const int32_t* table = p.pg.page_table + (size_t)b * p.pg.max_pages;
+      const int tiles = last - first - (GK * (last - 1) + T * warp >= L ? 1 : 0);
+      const TileCopy<D, Q4> copy(p.pg, hk, ring, lane);
+      int next_j = GK * first + T * warp;  // the first key of the next tile to be copied
+      int page_i = next_j / ps, slot = next_j - page_i * ps;
+      int page = tiles > 0 ? __ldg(table + page_i) : 0, page2 = 0;
+      auto second = [&]() { return slot + 16 >= ps ? page_i + 1 : page_i; };  // the second half's page index
+      if (paired && tiles > 0 && next_j + 16 < L) page2 = __ldg(table + second());
+      int left = tiles;      // to be copied
+      uint32_t copy_at = 0;  // the stage of the next one
+      uint32_t valid = 0;    // two bits for each of the last tiles copied: the halves that are there
+      auto issue = [&]() {
+        valid *= 4;
+        if (left > 0) {
+          --left;
+          const bool ok = (unsigned)page < (unsigned)p.pg.num_pages;
+          bool bad = !ok;
+          if (!paired) {
+            if (ok) copy.template rows<T / 16>(page, slot, copy_at, 0);
+            valid += ok ? 3u : 0u;
+          } else {
+            if (ok) copy.template rows<1>(page, slot, copy_at, 0);
+            valid += ok ? 1u : 0u;
+            if (next_j + 16 < L) {
+              const bool ok2 = (unsigned)page2 < (unsigned)p.pg.num_pages;
+              if (ok2) copy.template rows<1>(page2, slot + 16 >= ps ? slot + 16 - ps : slot + 16, copy_at, 1);
+              valid += ok2 ? 2u : 0u;
+              bad = bad || !ok2;
+            }
+          }
+          if (bad && lane == 0) record_status(1);
+          next_j += GK;
+          page_i += step_pages;
+          slot += step_slots;
+          if (slot >= ps) {
+            slot -= ps;
+            ++page_i;
+          }
+          if (left > 0) {
+            page = __ldg(table + page_i);
+            if (paired && next_j + 16 < L) page2 = __ldg(table + second());
+          }
+        }
+        copy_at = copy_at == (S - 1) * Cfg::kTileBytes ? 0 : copy_at + Cfg::kTileBytes;
+        cp_async_commit();
+      };
+  #pragma unroll
+      for (int s = 0; s < S - 1; ++s) issue();
+
+      Rows rows;
+      rows.init(p, b, hk, r0, L, lane);
+      uint32_t tile = ring + (S - 1) * Cfg::kTileBytes;
+      int j0 = GK * (first - 1) + T * warp;
+  #pragma unroll 1
+      for (int it = 0; it < tiles; ++it) {
+        cp_async_wait<S - 2>();
+        __syncwarp();  // the tile is here for every lane, and every lane is done with the one before
+        const uint32_t flags = (valid >> (2 * (S - 2))) & 3u;
+        issue();
+        tile = tile == ring + (S - 1) * Cfg::kTileBytes ? ring : tile + Cfg::kTileBytes;
+        j0 += GK;
+        if (flags != 0u) rows.step(tile, j0, flags);
+      }
+      cp_async_wait<0>();
+      __syncthreads();  // every warp is done with its ring: the memory now holds the warps' partial outputs
+  #pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+  #pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int r = 8 * nt + 2 * (lane & 3) + u;
+          float x = rows.l[nt][u];
+  #pragma unroll
+          for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+          if (lane < 4) {
+            s_m[warp][r] = rows.m[nt][u];
+            s_l[warp][r] = x;
+          }
+          rows.store(s_o + (warp * ROWS + r) * Cfg::kPitch, nt, u);
+        }
+      __syncthreads();
+  // ---- the block's: a warp per row, d/32 features per lane
+#pragma unroll 1
+  for (int r = warp; r < ROWS && r0 + r < p.R; r += kPagedWarps) {
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kPagedWarps; ++w) M = fmaxf(M, s_m[w][r]);
+    float ell = 0.f, acc[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) acc[j] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kPagedWarps; ++w) {
+      const float a = join_weight(s_m[w][r], M);
+      ell = fmaf(s_l[w][r], a, ell);
+#pragma unroll
+      for (int j = 0; j < W; ++j) acc[j] = fmaf(s_o[(w * ROWS + r) * Cfg::kPitch + 32 * j + lane], a, acc[j]);
+    }
+    emit(r, M, ell, acc);
+  }
+}
+
+// Output and log-sum-exp of a row from its maximum, sum and output, d/32 features a lane.
+template <int D, bool BF16>
+__device__ __forceinline__ void finish_row(const PagedParams& p, size_t row, int lane, float M, float ell, const float (&acc)[D / 32]) {
+  const float inv = ell == 0.f ? 0.f : 1.f / ell;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) store_out<D, BF16>(p.o, row * D + 32 * j + lane, acc[j] * inv);
+  if (lane == 0) p.lse[row] = ell == 0.f ? -INFINITY : (M + log2f(ell)) * 0.69314718055994531f;
+}
+
+template <int D, bool BF16, bool Q4, int NT>
+__global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlocks)) fa_paged_split_kernel(const PagedParams p) {
+  using Cfg = PagedConfig<D, Q4, NT>;
+  constexpr int W = D / 32, ROWS = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31;
+  const int units = p.pg.Hk * p.tiles;  // of one sequence
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int step_pages = GK / ps, step_slots = GK - step_pages * ps;
 
   // ---- this block's run of granules
   const GranuleScan scan = scan_granules(p);
@@ -902,113 +1025,13 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
     const int last = (int)min((long long)n, first + (end - at));  // granules first .. last − 1 of this unit
     const int hk = unit % p.pg.Hk, r0 = (unit / p.pg.Hk) * ROWS;
 
-    // ---- the warp's tiles, keys GK·i + T·warp on; page lookups run one tile ahead of the copies
-    const int32_t* table = p.pg.page_table + (size_t)b * p.pg.max_pages;
-    const int tiles = last - first - (GK * (last - 1) + T * warp >= L ? 1 : 0);
-    const TileCopy<D, Q4> copy(p.pg, hk, ring, lane);
-    int next_j = GK * first + T * warp;  // the first key of the next tile to be copied
-    int page_i = next_j / ps, slot = next_j - page_i * ps;
-    int page = tiles > 0 ? __ldg(table + page_i) : 0, page2 = 0;
-    auto second = [&]() { return slot + 16 >= ps ? page_i + 1 : page_i; };  // the second half's page index
-    if (paired && tiles > 0 && next_j + 16 < L) page2 = __ldg(table + second());
-    int left = tiles;      // to be copied
-    uint32_t copy_at = 0;  // the stage of the next one
-    uint32_t valid = 0;    // two bits for each of the last tiles copied: the halves that are there
-    auto issue = [&]() {
-      valid *= 4;
-      if (left > 0) {
-        --left;
-        const bool ok = (unsigned)page < (unsigned)p.pg.num_pages;
-        bool bad = !ok;
-        if (!paired) {
-          if (ok) copy.template rows<T / 16>(page, slot, copy_at, 0);
-          valid += ok ? 3u : 0u;
-        } else {
-          if (ok) copy.template rows<1>(page, slot, copy_at, 0);
-          valid += ok ? 1u : 0u;
-          if (next_j + 16 < L) {
-            const bool ok2 = (unsigned)page2 < (unsigned)p.pg.num_pages;
-            if (ok2) copy.template rows<1>(page2, slot + 16 >= ps ? slot + 16 - ps : slot + 16, copy_at, 1);
-            valid += ok2 ? 2u : 0u;
-            bad = bad || !ok2;
-          }
-        }
-        if (bad && lane == 0) record_status(1);
-        next_j += GK;
-        page_i += step_pages;
-        slot += step_slots;
-        if (slot >= ps) {
-          slot -= ps;
-          ++page_i;
-        }
-        if (left > 0) {
-          page = __ldg(table + page_i);
-          if (paired && next_j + 16 < L) page2 = __ldg(table + second());
-        }
-      }
-      copy_at = copy_at == (S - 1) * Cfg::kTileBytes ? 0 : copy_at + Cfg::kTileBytes;
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < S - 1; ++s) issue();
-
-    Rows rows;
-    rows.init(p, b, hk, r0, L, lane);
-    uint32_t tile = ring + (S - 1) * Cfg::kTileBytes;
-    int j0 = GK * (first - 1) + T * warp;
-#pragma unroll 1
-    for (int it = 0; it < tiles; ++it) {
-      cp_async_wait<S - 2>();
-      __syncwarp();  // the tile is here for every lane, and every lane is done with the one before
-      const uint32_t flags = (valid >> (2 * (S - 2))) & 3u;
-      issue();
-      tile = tile == ring + (S - 1) * Cfg::kTileBytes ? ring : tile + Cfg::kTileBytes;
-      j0 += GK;
-      if (flags != 0u) rows.step(tile, j0, flags);
-    }
-    cp_async_wait<0>();
-    __syncthreads();  // every warp is done with its ring: the memory now holds the warps' partial outputs
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int r = 8 * nt + 2 * (lane & 3) + u;
-        float x = rows.l[nt][u];
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-        if (lane < 4) {
-          s_m[warp][r] = rows.m[nt][u];
-          s_l[warp][r] = x;
-        }
-        rows.store(s_o + (warp * ROWS + r) * Cfg::kPitch, nt, u);
-      }
-    __syncthreads();
-    // ---- the block's: a warp per row, d/32 features per lane
     const bool whole = first == 0 && last == n;
     const int part = 2 * blockIdx.x + (first == 0 ? 1 : 0);
     if (first == 0 && last < n && threadIdx.x == 0)  // the blocks behind this one hold the rest
       p.units[blockIdx.x] = make_int4(b, hk, r0, 1 + (int)quotient(n - last + share - 1, share));
-#pragma unroll 1
-    for (int r = warp; r < ROWS && r0 + r < p.R; r += kPagedWarps) {
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kPagedWarps; ++w) M = fmaxf(M, s_m[w][r]);
-      float ell = 0.f, acc[W];
-#pragma unroll
-      for (int j = 0; j < W; ++j) acc[j] = 0.f;
-#pragma unroll
-      for (int w = 0; w < kPagedWarps; ++w) {
-        const float a = join_weight(s_m[w][r], M);
-        ell = fmaf(s_l[w][r], a, ell);
-#pragma unroll
-        for (int j = 0; j < W; ++j) acc[j] = fmaf(s_o[(w * ROWS + r) * Cfg::kPitch + 32 * j + lane], a, acc[j]);
-      }
+    run_piece<D, BF16, Q4, NT>(p, smem, b, hk, r0, L, first, last, [&](int r, float M, float ell, const float (&acc)[W]) {
       if (whole) {
-        const size_t row = paged_row(p, b, hk, r0 + r);
-        const float inv = ell == 0.f ? 0.f : 1.f / ell;
-#pragma unroll
-        for (int j = 0; j < W; ++j) store_out<D, BF16>(p.o, row * D + 32 * j + lane, acc[j] * inv);
-        if (lane == 0) p.lse[row] = ell == 0.f ? -INFINITY : (M + log2f(ell)) * 0.69314718055994531f;
+        finish_row<D, BF16>(p, paged_row(p, b, hk, r0 + r), lane, M, ell, acc);
       } else {
         const size_t row = (size_t)part * ROWS + r;
 #pragma unroll
@@ -1018,7 +1041,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
           p.part_ml[2 * row + 1] = ell;
         }
       }
-    }
+    });
     // ---- the next unit
     at += last - first;
     if (at >= end) break;
@@ -1033,6 +1056,61 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
       n = granules(p, L);
     }
   }
+}
+
+// The same for small calls in one kernel without a workspace: a cluster of blocks takes a unit, each block a share of its
+// granules, and joins the blocks' parts through distributed shared memory.
+template <int D, bool BF16, bool Q4, int NT>
+__global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlocks)) fa_paged_cluster_kernel(const PagedParams p) {
+  namespace cg = cooperative_groups;
+  using Cfg = PagedConfig<D, Q4, NT>;
+  constexpr int W = D / 32, ROWS = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_ml[ROWS][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int units = p.pg.Hk * p.tiles, u = blockIdx.x / C, b = u / units, unit = u - b * units;
+  const int hk = unit % p.pg.Hk, r0 = (unit / p.pg.Hk) * ROWS;
+  const int L = paged_length(p, b), n = granules(p, L);
+  if (L < 0 && unit == 0 && rank == 0 && threadIdx.x == 0) record_status(1);
+  const int share = (n + C - 1) / C, first = min(n, rank * share), last = min(n, first + share);
+  float* s_o = reinterpret_cast<float*>(smem);
+  run_piece<D, BF16, Q4, NT>(p, smem, b, hk, r0, L, first, last, [&](int r, float M, float ell, const float (&acc)[W]) {
+    if (C == 1) {
+      if (L >= 0) finish_row<D, BF16>(p, paged_row(p, b, hk, r0 + r), lane, M, ell, acc);
+      return;
+    }
+    // in the place of the first warp's part, which this lane has read
+#pragma unroll
+    for (int j = 0; j < W; ++j) s_o[r * Cfg::kPitch + 32 * j + lane] = acc[j];
+    if (lane == 0) {
+      s_ml[r][0] = M;
+      s_ml[r][1] = ell;
+    }
+  });
+  if (C == 1) return;
+  cluster.sync();
+  if (L >= 0) {
+    for (int r = rank + C * warp; r < ROWS && r0 + r < p.R; r += C * kPagedWarps) {
+      float M = -INFINITY;
+      for (int c = 0; c < C; ++c) M = fmaxf(M, cluster.map_shared_rank(&s_ml[r][0], c)[0]);
+      float ell = 0.f, acc[W];
+#pragma unroll
+      for (int j = 0; j < W; ++j) acc[j] = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < C; ++c) {
+        const float* ml = cluster.map_shared_rank(&s_ml[r][0], c);
+        const float* part = cluster.map_shared_rank(s_o + r * Cfg::kPitch, c);
+        const float a = join_weight(ml[0], M);
+        ell = fmaf(ml[1], a, ell);
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc[j] = fmaf(part[32 * j + lane], a, acc[j]);
+      }
+      finish_row<D, BF16>(p, paged_row(p, b, hk, r0 + r), lane, M, ell, acc);
+    }
+  }
+  cluster.sync();  // no block's shared memory goes while another reads it
 }
 
 // Block (worker, row of a tile): joins that row of the unit whose first part the worker holds.
@@ -1084,8 +1162,22 @@ static int paged_workers(int B, int Hk, int tiles, int Nk, int granule, int per_
   return (int)std::min<long long>(most, (long long)kSmCount * per_sm);
 }
 
+// Blocks of a cluster that takes one unit (128 keys a block, at most eight blocks), 0 where the keys are dealt out instead.
+// Clusters need all their blocks on the GPU at once, and leave it idle where they are few and the keys many.  us of one
+// sequence of 8 key heads (64 blocks), 16 bits, clusters and dealt out: 4096 keys 10.3 and 11.4, 8192 keys 15.4 and 13.1;
+// of two sequences (128 blocks): 8192 keys 18.5 and 20.6, 16384 keys 30.3 and 31.1; of four: 44.9 and 49.9.
+static int paged_cluster(int B, int Hk, int tiles, int Nk) {
+  const int C = std::min(8, (Nk + 127) / 128);
+  const long long blocks = (long long)B * Hk * tiles * C;
+  return blocks <= 2 * kSmCount && Nk <= (blocks >= 128 ? 16384 : 4096) ? C : 0;
+}
+
 void paged_workspace(int B, int Nq, int H, int Hk, int Nk, int d, size_t* o_bytes, size_t* ml_bytes, size_t* unit_bytes) {
   const int R = H / Hk * Nq, rows = paged_tile_rows(R), tiles = (R + rows - 1) / rows;
+  if (paged_cluster(B, Hk, tiles, Nk) > 0) {
+    *o_bytes = *ml_bytes = *unit_bytes = 0;
+    return;
+  }
   const size_t workers = paged_workers(B, Hk, tiles, Nk, granule_keys(false), 4), slots = 2 * workers * rows;
   *unit_bytes = workers * sizeof(int4);
   *o_bytes = slots * d * sizeof(float);
@@ -1095,10 +1187,27 @@ void paged_workspace(int B, int Nq, int H, int Hk, int Nk, int d, size_t* o_byte
 template <int D, bool BF16, bool Q4, int NT>
 static cudaError_t launch_paged_v(PagedParams p, int B, int Nk, cudaStream_t stream) {
   using Cfg = PagedConfig<D, Q4, NT>;
-  static std::atomic<unsigned long long> done{0};
-  cudaError_t e = set_smem_once(done, reinterpret_cast<const void*>(fa_paged_split_kernel<D, BF16, Q4, NT>), Cfg::kSmem);
-  if (e != cudaSuccess) return e;
+  static std::atomic<unsigned long long> done[2] = {{0}, {0}};
   p.granule = Cfg::kGranule;
+  const int C = paged_cluster(B, p.pg.Hk, p.tiles, Nk);
+  const void* kernel = C > 0 ? reinterpret_cast<const void*>(fa_paged_cluster_kernel<D, BF16, Q4, NT>)
+                             : reinterpret_cast<const void*>(fa_paged_split_kernel<D, BF16, Q4, NT>);
+  cudaError_t e = set_smem_once(done[C > 0], kernel, Cfg::kSmem);
+  if (e != cudaSuccess) return e;
+  if (C > 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(B * p.pg.Hk * p.tiles * C));
+    cfg.blockDim = dim3(kPagedThreads);
+    cfg.dynamicSmemBytes = Cfg::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fa_paged_cluster_kernel<D, BF16, Q4, NT>, p);
+  }
   p.workers = paged_workers(B, p.pg.Hk, p.tiles, Nk, Cfg::kGranule, Cfg::kBlocks);
   fa_paged_split_kernel<D, BF16, Q4, NT><<<p.workers, kPagedThreads, Cfg::kSmem, stream>>>(p);
   e = cudaPeekAtLastError();

@@ -238,10 +238,10 @@ int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, voi
   if (Nq < 1 || H < 1 || Nk < 1 || H % Hk != 0 || !std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
   if (!paged_sizes(B, Nq, H, Hk, Nk, d)) return FA_ERR_UNSUPPORTED;
   const long long rows = (long long)(H / Hk) * Nq;
-  if (B > 65535 || rows > 0x3fffffffLL || (rows + 15) / 16 * Hk > 65535) return FA_ERR_UNSUPPORTED;  // grid y, z
+  if (B > 65535 || rows > 0x3fffffffLL || (rows + 15) / 16 * Hk > 65535) return FA_ERR_UNSUPPORTED;  // units in 32 bits
   size_t ml_at, units_at;
   const size_t need = decode_paged_workspace(B, Nq, H, Hk, Nk, d, &ml_at, &units_at);
-  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes_ < need)
+  if (need > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes_ < need))
     return FA_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const PagedDecodeArgs a = {q, o, lse, reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + ml_at), ws + units_at, Nq, H, Nk, scale};

@@ -491,8 +491,10 @@ int fa_cache_gather(const void* k_cache, const void* v_cache, void* k, void* v, 
  * of o infinite or NaN.
  * The scores and sums are fp32; P carries two 16-bit parts into the product with
  * V (4-bit cache: one fp16 part of P times the value's scale).  The workspace
- * holds the parts of chunks of keys, as in fa_decode; a 256-byte aligned buffer of
- * fa_decode_paged_workspace_bytes(...) bytes.  A sequence whose length is out of
+ * holds the parts of runs of keys; a 256-byte aligned buffer of
+ * fa_decode_paged_workspace_bytes(...) bytes, contents irrelevant (calls that may run at
+ * the same time need one each), or NULL where that
+ * is 0: small calls (at most 16384 keys, few sequences and heads) need none.  A sequence whose length is out of
  * range is skipped, its rows of o and lse left as they are.
  */
 size_t fa_decode_paged_workspace_bytes(int B, int Nq, int H, int Hk, int Nk, int d);

@@ -81,7 +81,14 @@ def _cache(lens, hk, d, page, dtype, bits, seed, spread=1.0):
     return table, out[0], out[1]
 
 
-def _check_decode(fa, lens, nq, H, hk, d, page, dtype, bits, seed=0, scale=None, max_len=None, spread=1.0):
+def _check_decode(fa, lens, nq, H, hk, d, page, dtype, bits, seed=0, scale=None, spread=1.0):
+    """With the bound that the table gives (small calls: a cluster of blocks per key head) and with a wide one (the keys dealt
+    out over all blocks)."""
+    for max_len in (None, 100000):
+        _check_decode_bounded(fa, lens, nq, H, hk, d, page, dtype, bits, seed, scale, max_len, spread)
+
+
+def _check_decode_bounded(fa, lens, nq, H, hk, d, page, dtype, bits, seed, scale, max_len, spread):
     table, kc, vc = _cache(lens, hk, d, page, dtype, bits, seed, spread)
     g = torch.Generator().manual_seed(seed + 1)
     q = torch.randn(len(lens), nq, H, d, generator=g).to(DT[dtype])
@@ -141,6 +148,14 @@ def test_decode_heads_and_pages(fa, heads, page, bits):
 def test_decode_several_tokens(fa, d, nq, bits):
     """Lengths under the number of tokens leave the first rows without a key."""
     _check_decode(fa, [nq, nq - 1, 1, 0, 16, 33, 200], nq, 4, 2, d, 32, "fp16", bits, seed=nq)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("n", [127, 128, 129, 256, 900, 1024, 1025, 4096, 4097])
+def test_decode_cluster_borders(fa, n, bits):
+    """One block, two, all eight of a cluster, blocks without keys, and one key past the largest cluster call."""
+    _check_decode(fa, [n], 1, 4, 2, 64, 64, "bf16", bits, seed=n)
+    _check_decode(fa, [1, n, 0], 3, 4, 1, 128, 16, "fp16", bits, seed=n + 1)
 
 
 @pytest.mark.parametrize("bits", [16, 4])
@@ -526,7 +541,7 @@ def test_decode_matches_the_contiguous_decode(fa):
 
 
 def test_decode_repeats_captured_shared_workspace_and_streams(fa):
-    lens = [600, 3000, 1]
+    lens = [600, 5000, 1]
     table, kc, vc = (t.cuda() for t in _cache(lens, 2, 128, 64, "bf16", 4, 21))
     ln = torch.tensor(lens, dtype=torch.int32).cuda()
     q = torch.randn(3, 8, 128, generator=torch.Generator().manual_seed(7)).bfloat16().cuda()

@@ -93,8 +93,8 @@ def test_cache_gather_refusals(fa):
 
 
 def test_decode_paged_refusals(fa):
-    ws = fa.fa_decode_paged_workspace_bytes(2, 1, 4, 2, 32, 64)
-    good = dict(q=P16, k_cache=P16, v_cache=P16, o=P16, lse=P16, page_table=P16, seqlens_k=P16, B=2, Nq=1, H=4, Hk=2, Nk=32, d=64,
+    ws = fa.fa_decode_paged_workspace_bytes(2, 1, 4, 2, 40960, 64)
+    good = dict(q=P16, k_cache=P16, v_cache=P16, o=P16, lse=P16, page_table=P16, seqlens_k=P16, B=2, Nq=1, H=4, Hk=2, Nk=40960, d=64,
                 scale=0.125, page_size=16, num_pages=3, max_pages=2, dtype=0, cache_format=0, workspace=P16, workspace_bytes=ws,
                 stream=None)
     _check(fa.fa_decode_paged, good, CACHE_BAD + [
@@ -113,9 +113,12 @@ def test_sizes(fa):
     assert fa.fa_cache_bytes(3, 16, 2, 64, 2) == 0
     assert fa.fa_decode_paged_workspace_bytes(1, 1, 4, 3, 64, 64) == 0
     assert fa.fa_decode_paged_workspace_bytes(1, 1, 4, 2, 0, 64) == 0
-    # one part of every row and chunk at most, whatever the length
-    for nk in (1, 100, 5000, 131072, 1 << 30):
-        assert 0 < fa.fa_decode_paged_workspace_bytes(1, 1, 8, 8, nk, 128) < 1 << 31
+    # two parts of each block at most, whatever the length; small calls need none
+    for nk in (1, 100, 4096):
+        assert fa.fa_decode_paged_workspace_bytes(1, 1, 8, 8, nk, 128) == 0
+    for nk in (4097, 5000, 131072, 1 << 30):
+        assert 0 < fa.fa_decode_paged_workspace_bytes(1, 1, 8, 8, nk, 128) < 1 << 25
+    assert fa.fa_decode_paged_workspace_bytes(64, 1, 8, 8, 2048, 128) > 0
 
 
 def test_wrapper_refusals(fa):
@@ -136,3 +139,21 @@ def test_wrapper_refusals(fa):
             call()
     with pytest.raises(AttributeError):
         fa.attention_no_such_thing
+
+
+def test_missing_binding_fails_loudly(fa, tmp_path):
+    """No fallback: without the binding the wrappers cannot be had, while the library itself still loads."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+    pkg = os.path.dirname(fa.__file__)
+    dst = tmp_path / os.path.basename(pkg)
+    os.makedirs(dst)
+    for f in ("__init__.py", "paged.py", "libfa_b200.so"):
+        shutil.copy(os.path.join(pkg, f), dst / f)
+    code = (f"import {dst.name} as fa\nprint(fa.fa_version())\n"
+            "try:\n    fa.attention_cache_append\nexcept ImportError as e:\n    print('refused:', e)\n")
+    out = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stderr[-500:]
+    assert "sm_100a" in out.stdout and "refused: the torch binding is missing" in out.stdout
