@@ -20,7 +20,7 @@ BINDING_PATH = os.path.join(HERE, "_binding.so")
 SOURCES = ["libfa_b200.cu"]
 DEPS = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu", "fa_merge.cu", "fa_noalloc.cu", "fa_rope.cu",
         "fa_cache.cu", "fa_paged.cu", "fa_paged_api.cu"]
-HEADERS = ["fa_internal.h", "sm100.cuh", "rope.cuh", "paged.cuh", os.path.join("..", "..", "include", "fa.h")]
+HEADERS = ["fa_internal.h", "sm100.cuh", "fa_paged_internal.h", "async_copy.cuh", "rope.cuh", "paged.cuh", os.path.join("..", "..", "include", "fa.h")]
 
 
 def nvcc_path() -> str:

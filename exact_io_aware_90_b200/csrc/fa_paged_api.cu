@@ -5,7 +5,7 @@
 #include <cmath>
 
 #include "../../include/fa.h"
-#include "fa_internal.h"
+#include "fa_paged_internal.h"
 
 namespace fa {
 

@@ -11,7 +11,8 @@
 //   value  feature 32w + 4g + n (g < 8, n < 4): nibble n of 16-bit word g·W + w
 #pragma once
 
-#include "fa_internal.h"
+#include "async_copy.cuh"
+#include "fa_paged_internal.h"
 #include "sm100.cuh"
 
 namespace fa {

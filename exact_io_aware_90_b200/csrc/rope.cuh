@@ -12,7 +12,7 @@
 // unrotated features each.
 #pragma once
 
-#include "fa_internal.h"
+#include "fa_paged_internal.h"
 #include "sm100.cuh"
 
 namespace fa {

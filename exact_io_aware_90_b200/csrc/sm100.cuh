@@ -508,16 +508,6 @@ __device__ __forceinline__ void regs_set() {
   else if constexpr (N < LAUNCH) regs_dec<N>();
 }
 
-// ---------------------------------------------------------------- asynchronous 16-byte copies
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // ---------------------------------------------------------------- small math
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float r;
