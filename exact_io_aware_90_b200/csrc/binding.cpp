@@ -139,6 +139,7 @@ struct Place {
       PyObject* o = a.next();
       void* p = PyLong_AsVoidPtr(o);
       if (p == nullptr && PyErr_Occurred()) throw PythonError{};
+      if (p == cudaStreamLegacy) p = nullptr;  // the default stream, which torch knows as 0
       stream = static_cast<cudaStream_t>(p);
       own.emplace(c10::cuda::getStreamFromExternal(stream, d.index()));
     }

@@ -34,7 +34,8 @@
 // a chain of lookups and copies).
 //
 // The reference of the exponents rises only when a score passes it by 2^8 (one vote per tile).  P of 16-bit caches is
-// the sum of two 16-bit parts, so its rounding stays behind the output's.
+// the sum of two 16-bit parts, so its rounding stays behind the output's; in fp16 the reference is 2^7 below the maximum,
+// so that P, up to 2^15, keeps keys down to 2^-32 of the largest (many of them may outweigh it).
 //
 // 4 bits.  Instructions bound this path (16 keys by 8 rows of d = 128 have 2,560 bytes to read and 4,096 numbers to unpack;
 // 347 instructions per warp, 52 % of the issue slots with three warps per scheduler, the integer pipe 45 % busy, HBM 70 %),
@@ -326,6 +327,7 @@ struct TileCopy {
 template <int D, bool BF16, int NT>
 struct Rows16 {
   static constexpr int W = D / 32, KS = D / 16, ROW = D * 2;
+  static constexpr float kDepth = BF16 ? 0.f : 7.f;  // how far the reference is under the maximum
   uint32_t qb[NT][KS][2];
   float m[NT][2], mz[NT][2], rise_at[NT][2];  // the reference, with 0 for −inf, and the dot product from which it has to rise
   float l[NT][2], o[NT][KS][4];
@@ -411,11 +413,11 @@ struct Rows16 {
           float x = fmaxf(s[nt][u], s[nt][2 + u]);
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-          const float mn = fmaxf(m[nt][u], x * coef);
+          const float mn = fmaxf(m[nt][u], fmaf(x, coef, -kDepth));
           const float alpha = m[nt][u] == -INFINITY ? 0.f : ex2(m[nt][u] - mn);
           m[nt][u] = mn;
           mz[nt][u] = mn == -INFINITY ? 0.f : mn;
-          rise_at[nt][u] = (mn + kRise) / coef;
+          rise_at[nt][u] = (mn + (kDepth + kRise)) / coef;
           l[nt][u] *= alpha;
 #pragma unroll
           for (int j = 0; j < KS; ++j) {

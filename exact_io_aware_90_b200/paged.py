@@ -31,7 +31,7 @@ def attention_rope_table(rows: int, rot_dim: int, base: float = 10000.0, device=
     with torch.cuda.device(device):
         if stream is None:
             stream = torch.cuda.current_stream().cuda_stream
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream)):
+        with torch.cuda.stream(torch.cuda.ExternalStream(0 if stream == 1 else stream)):  # 1: the default stream too
             cos, sin = (torch.empty((rows, rot_dim // 2), dtype=torch.float32, device="cuda") for _ in range(2))
         st = lib.fa_rope_table(cos.data_ptr(), sin.data_ptr(), rows, rot_dim, float(base), stream)
     if st != FA_OK:

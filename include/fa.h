@@ -431,7 +431,8 @@ int fa_rope_table(float* cos_t, float* sin_t, int table_rows, int rot_dim, doubl
  * A 4-bit row is made from the row rounded to the dtype: min = the least of the 32
  * values in fp16, scale = (largest − least)/15 in fp16 (both kept within ±65504),
  * n = (value − min)/scale rounded to nearest even and kept within 0..15 (0 when
- * scale is 0).
+ * scale is 0).  Such a row is finite: an infinity becomes the largest or least of
+ * its 32, a NaN counts for neither and becomes the least.
  * What the device finds out of range (lengths, offsets, pages, positions) records
  * FA_ERR_INVALID_ARG in the device status word and is skipped; nothing outside the
  * caches is touched.
@@ -455,7 +456,7 @@ size_t fa_cache_bytes(int num_pages, int page_size, int Hk, int d, int cache_for
  *   positions    int32 [axes, T]; NULL (axes = 1): the position in the sequence
  *   cos_t, sin_t both NULL: no rotation
  * Rows behind the last sequence are left as they are, and so are q_out's.  Two
- * tokens with the same page and slot are written in an undefined order.
+ * tokens with the same page and slot leave there a mixture of the two.
  */
 int fa_cache_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache, void* v_cache,
                     const void* wq, const void* wk, const float* cos_t, const float* sin_t, const int32_t* positions,
@@ -488,7 +489,8 @@ int fa_cache_gather(const void* k_cache, const void* v_cache, void* k, void* v, 
  *                lengths above max_pages·page_size are out of range too
  * H a multiple of Hk.  Keys and values that a query does not see may hold anything
  * (infinities, NaN); an infinity or NaN in a value that it sees makes that feature
- * of o infinite or NaN.
+ * of o infinite or NaN.  (4 bits: the scales and minima of the sequence's keys are
+ * finite, as fa_cache_append leaves them.)
  * The scores and sums are fp32; P carries two 16-bit parts into the product with
  * V (4-bit cache: one fp16 part of P times the value's scale).  The workspace
  * holds the parts of runs of keys; a 256-byte aligned buffer of

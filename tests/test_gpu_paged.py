@@ -181,6 +181,43 @@ def test_decode_large_scores_and_unlike_scales(fa, bits):
     _check_decode(fa, [900], 1, 4, 2, 64, 64, "fp16", bits, seed=7, spread=6.0)
 
 
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("at", [0, 900, 2999])
+def test_decode_one_key_far_above_the_rest(fa, at, dtype, d, bits):
+    """One key whose value is 0 scores 18 above all others, which are 2^-26 of it each: the output is theirs alone.  What a
+    16-bit P adds to the module's bound: each key is off by 2^-25 beside a largest of at least 2^7, 2^-32 of it."""
+    n, page = 3000, 64
+    g = torch.Generator().manual_seed(30)
+    table, total = _table([n], page, g)
+    k = torch.zeros(total, 1, page, d)
+    v = torch.rand(total, 1, page, d, generator=g) + 1.0
+    k[int(table[0, at // page]), 0, at % page, 0] = 18.0
+    v[int(table[0, at // page]), 0, at % page] = 0.0
+    k, v = k.to(DT[dtype]), v.to(DT[dtype])
+    kc, vc = (k, v) if bits == 16 else (_pack(k, False), _pack(v, True))
+    q = torch.zeros(1, 1, d)
+    q[..., 0] = 1.0
+    kr, ka, km, _ = oracle.cache_rows(kc, table.numpy(), 0, np.arange(n), d, False)
+    vr, va, vm, vs = oracle.cache_rows(vc, table.numpy(), 0, np.arange(n), d, True)
+    ref, rl = oracle.decode_paged(f64(q), kr, vr, 1.0)
+    p = np.exp(kr[:, 0, 0] - rl[0, 0])
+    ds = 2.0 ** -18 * 18 + 2.0 ** -22 * 18
+    bound = (p @ np.abs(vr[:, 0])) * (2 * ds + 2.0 ** -16) + torch.finfo(DT[dtype]).eps / 2 * np.abs(ref[0, 0]) * (1 + 2.0 ** -7)
+    bound = bound + 2.0 ** -25 + 2.0 ** -32 * p.max() * np.abs(vr[:, 0]).sum(0)
+    if bits == 4:  # P times the scale is rounded too
+        bound = bound + (p @ np.abs(va[:, 0])) * 2.0 ** -11 + n * 15 * 2.0 ** -31 * (p.max() * vs.max())
+    assert np.abs(ref).min() > 4 * bound.max() if bits == 16 else True  # the bound tells the output from 0
+    for most in (None, 100000):
+        o, lse = fa.attention_decode_paged(q.to(DT[dtype]).cuda(), kc.cuda(), vc.cuda(), table.cuda(), torch.tensor([n], dtype=torch.int32).cuda(),
+                                           max_seqlen_k=most, scale=1.0)
+        err = np.abs(f64(o)[0, 0] - ref[0, 0])
+        assert np.all(err <= bound), (err / bound).max()
+        assert abs(f64(lse)[0, 0] - rl[0, 0]) <= ds + 2.0 ** -20 * (1 + abs(rl[0, 0]))
+    assert _status(fa) == fa.FA_OK
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_decode_q4_constant_and_tiny_rows(fa, dtype):
     """Groups without spread (scale 0), values near fp16's smallest and queries of unlike sizes."""
@@ -365,6 +402,34 @@ def test_append_extreme_values(fa):
     assert np.isfinite(sc).all() and np.isfinite(mn).all()
     rn, rs, rm = oracle.four_bit_rows(f64(x)[[0, 2, 3]])
     assert np.array_equal(n[0, 0, [0, 2, 3]], rn[:, 0]) and np.array_equal(sc[0, 0, [0, 2, 3]], rs[:, 0]) and np.array_equal(mn[0, 0, [0, 2, 3]], rm[:, 0])
+    assert _status(fa) == fa.FA_OK
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_append_q4_rows_are_finite(fa, value):
+    """An infinity becomes the largest or least number of its group, a NaN the least; the other groups are as without it."""
+    g = torch.Generator().manual_seed(31)
+    x = torch.randn(16, 2, 128, generator=g).bfloat16()
+    clean = x.clone()
+    at = torch.randint(32, (16, 2), generator=g)
+    for t in range(16):
+        for h in range(2):
+            x[t, h, 32 + int(at[t, h])] = value
+            # in the oracle's row the place holds the least value of the rest
+            clean[t, h, 32 + int(at[t, h])] = torch.cat([clean[t, h, 32:32 + int(at[t, h])], clean[t, h, 33 + int(at[t, h]):64]]).min()
+    n, sc, mn = oracle.four_bit_rows(f64(clean))
+    caches = [torch.zeros(1, 2, 16, 80, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    fa.attention_cache_append(x.cuda(), x.cuda(), *caches, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                              torch.tensor([16], dtype=torch.int32, device="cuda"))
+    for c, is_value in zip(caches, (False, True)):
+        gn, gs, gm = (y[0].swapaxes(0, 1) for y in oracle.four_bit_unpack(c.cpu().reshape(1, 2, -1).numpy(), 16, 128, is_value))
+        assert np.isfinite(gs).all() and np.isfinite(gm).all()
+        same = [0, 2, 3] if not math.isnan(value) else [0, 1, 2, 3]
+        assert np.array_equal(gs[..., same], sc[..., same]) and np.array_equal(gm[..., same], mn[..., same])
+        feat = np.concatenate([np.arange(32 * w, 32 * w + 32) for w in same])
+        assert np.array_equal(gn[..., feat], n[..., feat])
+        bad = np.take_along_axis(gn, 32 + at.numpy()[..., None], -1)
+        assert np.all(bad == (15 if value == math.inf else 0))
     assert _status(fa) == fa.FA_OK
 
 
