@@ -67,7 +67,10 @@ constexpr int kPagedWarps = 4;
 constexpr int kPagedThreads = 32 * kPagedWarps;
 constexpr float kRise = 8.f;  // how far a score may pass the reference before the reference follows
 
-// Tile, ring depth and blocks per SM of a variant: at least 40 KB in flight per SM (HBM latency times its share of the
+// Blocks per SM of a variant.
+constexpr int paged_blocks(int d, bool q4, int nt) { return d == 64 ? (nt == 2 ? 3 : 4) : nt == 2 || !q4 ? 2 : 3; }
+
+// Tile and ring depth of a variant: at least 40 KB in flight per SM (HBM latency times its share of the
 // bandwidth), within 227 KB of shared memory and the registers.
 template <int D, bool Q4, int NT>
 struct PagedConfig {
@@ -75,7 +78,7 @@ struct PagedConfig {
   static constexpr int kGranule = kTile * kPagedWarps;   // keys of all warps' tiles
   static constexpr int kTileBytes = kTile * (Q4 ? 2 * (D / 2 + D / 8) : 2 * D * 2);
   static constexpr int kStages = Q4 ? 2 : 3;
-  static constexpr int kBlocks = D == 64 ? (NT == 2 ? 3 : 4) : NT == 2 || !Q4 ? 2 : 3;
+  static constexpr int kBlocks = paged_blocks(D, Q4, NT);
   static constexpr int kRing = kPagedWarps * kStages * kTileBytes;
   static constexpr int kRows = 8 * NT;
   static constexpr int kPitch = D + 4;  // floats per row of the warps' partial outputs
@@ -93,7 +96,9 @@ struct PagedParams {
   PagedArgs pg;
   int Nq, H, G, most, R, tiles;  // G = H/Hk, most: the largest length allowed, R = G·Nq rows of a key head in `tiles` tiles
   int workers, granule;
-  int4* units;  // [workers]: for the block that holds the first part of a unit: sequence, key head, first row, parts (else 0)
+  bool by_unit;
+  int4* units;  // what the merge joins, for each unit (by_unit) or for each worker: sequence, unit of it, the worker that
+                // holds the first part, parts (0: nothing to join)
   float scale_log2;
 };
 
@@ -1020,8 +1025,10 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
       for (size_t i = threadIdx.x; i < rows * D; i += kPagedThreads) store_out<D, BF16>(p.o, b * rows * D + i, 0.f);
       for (size_t i = threadIdx.x; i < rows; i += kPagedThreads) p.lse[b * rows + i] = -INFINITY;
     }
+    if (len <= 0 && p.by_unit)
+      for (int i = threadIdx.x; i < units; i += kPagedThreads) p.units[b * units + i] = make_int4(0, 0, 0, 0);
   }
-  if (threadIdx.x == 0) p.units[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (threadIdx.x == 0 && !p.by_unit) p.units[blockIdx.x] = make_int4(0, 0, 0, 0);
   __syncthreads();
   if (at >= end) return;
   int b = s_b, L = paged_length(p, b), n = granules(p, L);
@@ -1035,8 +1042,9 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
 
     const bool whole = first == 0 && last == n;
     const int part = 2 * blockIdx.x + (first == 0 ? 1 : 0);
-    if (first == 0 && last < n && threadIdx.x == 0)  // the blocks behind this one hold the rest
-      p.units[blockIdx.x] = make_int4(b, hk, r0, 1 + (int)quotient(n - last + share - 1, share));
+    if (first == 0 && threadIdx.x == 0 && (p.by_unit || last < n))  // the blocks behind this one hold the rest
+      p.units[p.by_unit ? b * units + unit : (int)blockIdx.x] =
+          make_int4(b, unit, blockIdx.x, last < n ? 1 + (int)quotient(n - last + share - 1, share) : 0);
     run_piece<D, BF16, Q4, NT>(p, smem, b, hk, r0, L, first, last, [&](int r, float M, float ell, const float (&acc)[W]) {
       if (whole) {
         finish_row<D, BF16>(p, paged_row(p, b, hk, r0 + r), lane, M, ell, acc);
@@ -1121,16 +1129,16 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
   cluster.sync();  // no block's shared memory goes while another reads it
 }
 
-// Block (worker, row of a tile): joins that row of the unit whose first part the worker holds.
+// Block (note, row of a tile): joins that row of the unit, whose parts four warps share out.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p) {
   constexpr int F = D / 32;
   __shared__ float s_o[4][D], s_l[4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y, tile_rows = gridDim.y, w0 = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y, tile_rows = gridDim.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 unit = __ldcg(p.units + w0);  // sequence, key head, first row, parts
-  const int parts = unit.w;
-  if (parts == 0 || unit.z + r >= p.R) return;
+  const int4 note = __ldcg(p.units + blockIdx.x);  // sequence, unit of it, first worker, parts
+  const int hk = note.y % p.pg.Hk, row = note.y / p.pg.Hk * tile_rows + r, w0 = note.z, parts = note.w;
+  if (parts == 0 || row >= p.R) return;
   // the first worker's part is its last one (slot 1), the others' their first (slot 0)
   auto slot = [&](int i) { return (size_t)(2 * (w0 + i) + (i == 0 ? 1 : 0)) * tile_rows + r; };
   float M = -INFINITY;
@@ -1153,12 +1161,11 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p
   for (int j = 0; j < F; ++j) s_o[warp][32 * j + lane] = acc[j];
   if (lane == 0) s_l[warp] = ell;
   __syncthreads();
+  if (warp > 0) return;
   ell = s_l[0] + s_l[1] + s_l[2] + s_l[3];
-  const float inv = ell == 0.f ? 0.f : 1.f / ell;
-  const size_t row = paged_row(p, unit.x, unit.y, unit.z + r);
-  for (int f = threadIdx.x; f < D; f += 128)
-    store_out<D, BF16>(p.o, row * D + f, (s_o[0][f] + s_o[1][f] + s_o[2][f] + s_o[3][f]) * inv);
-  if (threadIdx.x == 0) p.lse[row] = ell == 0.f ? -INFINITY : (M + log2f(ell)) * 0.69314718055994531f;
+#pragma unroll
+  for (int j = 0; j < F; ++j) acc[j] = s_o[0][32 * j + lane] + s_o[1][32 * j + lane] + s_o[2][32 * j + lane] + s_o[3][32 * j + lane];
+  finish_row<D, BF16>(p, paged_row(p, note.x, hk, row), lane, M, ell, acc);
 }
 
 // Row tiles of a key head, and the rows of one.
@@ -1170,19 +1177,27 @@ static int paged_workers(int B, int Hk, int tiles, int Nk, int granule, int per_
   return (int)std::min<long long>(most, (long long)kSmCount * per_sm);
 }
 
-// Blocks of a cluster that takes one unit (128 keys a block, at most eight blocks), 0 where the keys are dealt out instead.
-// Clusters need all their blocks on the GPU at once, and leave it idle where they are few and the keys many.  us of one
-// sequence of 8 key heads (64 blocks), 16 bits, clusters and dealt out: 4096 keys 10.3 and 11.4, 8192 keys 15.4 and 13.1;
-// of two sequences (128 blocks): 8192 keys 18.5 and 20.6, 16384 keys 30.3 and 31.1; of four: 44.9 and 49.9.
-static int paged_cluster(int B, int Hk, int tiles, int Nk) {
-  const int C = std::min(8, (Nk + 127) / 128);
-  const long long blocks = (long long)B * Hk * tiles * C;
-  return blocks <= 2 * kSmCount && Nk <= (blocks >= 128 ? 16384 : 4096) ? C : 0;
+// Blocks of a cluster that takes one unit, 0 where the keys are dealt out instead.  Clusters need one launch and no second
+// pass over partial outputs, but a cluster's blocks have to be on the GPU at once and all units take as long as the longest.
+// As many blocks (1, 2, 4 or 8) as the keys fill (over 64 each) and the GPU holds beside one another (a sixteenth is left
+// because clusters do not pack); the keys are dealt out where a block would get more than 1024 of them (2048 where the
+// blocks fill the GPU).  Units that do not all fit at once take one block each up to 2048 keys.
+// us of batches with half to all of the given keys, 16 bits, d = 128, clusters and dealt out: 12 x 256 keys x 16 heads 6.8 and
+// 11.5; 37 x 512 x 4 heads of 20 rows 12.9 and 22.7; 37 x 1024 x 1 head of 16 rows 10.8 and 15.6; 1 x 4096 x
+// 8 heads 10.3 and 11.4; 4 x 8192 x 4 heads of 20 rows 21.5 and 25.6, but 1 x 8192 x 16 heads 17.3 and 15.9; 4 bits:
+// 37 x 2048 x 16 heads of 10 rows 56.3 and 64.3, 37 x 4096 x 16 heads of 1 row 83.9 and 68.8 (dealt out by the rule).
+static int paged_cluster(int B, int Hk, int tiles, int Nk, int per_sm) {
+  const long long units = (long long)B * Hk * tiles, room = kSmCount * per_sm * 15 / 16;
+  if (units > room) return Nk <= 2048 ? 1 : 0;
+  int C = 8;
+  while (C > 1 && (Nk <= 64 * C || units * C > room)) C /= 2;
+  return (Nk + C - 1) / C <= (10 * units * C >= 7 * room ? 2048 : 1024) ? C : 0;
 }
 
 void paged_workspace(int B, int Nq, int H, int Hk, int Nk, int d, size_t* o_bytes, size_t* ml_bytes, size_t* unit_bytes) {
   const int R = H / Hk * Nq, rows = paged_tile_rows(R), tiles = (R + rows - 1) / rows;
-  if (paged_cluster(B, Hk, tiles, Nk) > 0) {
+  const int nt = rows / 8;
+  if (paged_cluster(B, Hk, tiles, Nk, paged_blocks(d, false, nt)) > 0 && paged_cluster(B, Hk, tiles, Nk, paged_blocks(d, true, nt)) > 0) {
     *o_bytes = *ml_bytes = *unit_bytes = 0;
     return;
   }
@@ -1197,7 +1212,7 @@ static cudaError_t launch_paged_v(PagedParams p, int B, int Nk, cudaStream_t str
   using Cfg = PagedConfig<D, Q4, NT>;
   static std::atomic<unsigned long long> done[2] = {{0}, {0}};
   p.granule = Cfg::kGranule;
-  const int C = paged_cluster(B, p.pg.Hk, p.tiles, Nk);
+  const int C = paged_cluster(B, p.pg.Hk, p.tiles, Nk, Cfg::kBlocks);
   const void* kernel = C > 0 ? reinterpret_cast<const void*>(fa_paged_cluster_kernel<D, BF16, Q4, NT>)
                              : reinterpret_cast<const void*>(fa_paged_split_kernel<D, BF16, Q4, NT>);
   cudaError_t e = set_smem_once(done[C > 0], kernel, Cfg::kSmem);
@@ -1217,11 +1232,13 @@ static cudaError_t launch_paged_v(PagedParams p, int B, int Nk, cudaStream_t str
     return cudaLaunchKernelEx(&cfg, fa_paged_cluster_kernel<D, BF16, Q4, NT>, p);
   }
   p.workers = paged_workers(B, p.pg.Hk, p.tiles, Nk, Cfg::kGranule, Cfg::kBlocks);
+  p.by_unit = (long long)B * p.pg.Hk * p.tiles <= p.workers;
   fa_paged_split_kernel<D, BF16, Q4, NT><<<p.workers, kPagedThreads, Cfg::kSmem, stream>>>(p);
   e = cudaPeekAtLastError();
   if (e != cudaSuccess) return e;
   // the merge is launched while the runs end; it waits for them before it reads
-  return launch_after(fa_paged_merge_kernel<D, BF16>, dim3((unsigned)p.workers, 8 * NT), dim3(128), stream, p);
+  const unsigned notes = (unsigned)(p.by_unit ? B * p.pg.Hk * p.tiles : p.workers);
+  return launch_after(fa_paged_merge_kernel<D, BF16>, dim3(notes, 8 * NT), dim3(128), stream, p);
 }
 
 template <int D, bool BF16>
@@ -1247,6 +1264,7 @@ cudaError_t launch_decode_paged(const PagedDecodeArgs& a, const PagedArgs& pg, c
   p.R = p.G * a.Nq;
   p.tiles = (p.R + paged_tile_rows(p.R) - 1) / paged_tile_rows(p.R);
   p.workers = p.granule = 0;
+  p.by_unit = false;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   if (pg.d == 128) return pg.bf16 ? launch_paged_t<128, true>(p, pg.B, a.Nk, stream) : launch_paged_t<128, false>(p, pg.B, a.Nk, stream);
   return pg.bf16 ? launch_paged_t<64, true>(p, pg.B, a.Nk, stream) : launch_paged_t<64, false>(p, pg.B, a.Nk, stream);

@@ -496,8 +496,8 @@ int fa_cache_gather(const void* k_cache, const void* v_cache, void* k, void* v, 
  * holds the parts of runs of keys; a 256-byte aligned buffer of
  * fa_decode_paged_workspace_bytes(...) bytes, contents irrelevant (calls that may run at
  * the same time need one each), or NULL where that
- * is 0: small calls (at most 16384 keys, few sequences and heads) need none.  A sequence whose length is out of
- * range is skipped, its rows of o and lse left as they are.
+ * is 0: small calls need none.  A sequence whose length is out of range is skipped,
+ * its rows of o and lse left as they are.
  */
 size_t fa_decode_paged_workspace_bytes(int B, int Nq, int H, int Hk, int Nk, int d);
 int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,

@@ -151,11 +151,19 @@ def test_decode_several_tokens(fa, d, nq, bits):
 
 
 @pytest.mark.parametrize("bits", [16, 4])
-@pytest.mark.parametrize("n", [127, 128, 129, 256, 900, 1024, 1025, 4096, 4097])
+@pytest.mark.parametrize("n", [64, 127, 128, 129, 256, 257, 512, 513, 900, 1024, 1025, 4096, 4097, 8192, 8193])
 def test_decode_cluster_borders(fa, n, bits):
-    """One block, two, all eight of a cluster, blocks without keys, and one key past the largest cluster call."""
+    """One block, two, four, all eight of a cluster, blocks without keys, and one key past the largest cluster call."""
     _check_decode(fa, [n], 1, 4, 2, 64, 64, "bf16", bits, seed=n)
     _check_decode(fa, [1, n, 0], 3, 4, 1, 128, 16, "fp16", bits, seed=n + 1)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("seqs,hk,most", [(20, 8, 300), (40, 4, 130), (80, 8, 90)])
+def test_decode_many_units(fa, seqs, hk, most, bits):
+    """More units than clusters of eight have room for, and than blocks fit the GPU; dealt out, more than there are blocks."""
+    lens = np.random.default_rng(seqs).integers(0, most + 1, seqs).tolist()
+    _check_decode(fa, lens, 1, hk, hk, 64 if seqs == 40 else 128, 16, "bf16", bits, seed=seqs)
 
 
 @pytest.mark.parametrize("bits", [16, 4])
@@ -610,24 +618,25 @@ def test_decode_repeats_captured_shared_workspace_and_streams(fa):
     table, kc, vc = (t.cuda() for t in _cache(lens, 2, 128, 64, "bf16", 4, 21))
     ln = torch.tensor(lens, dtype=torch.int32).cuda()
     q = torch.randn(3, 8, 128, generator=torch.Generator().manual_seed(7)).bfloat16().cuda()
-    ref = fa.attention_decode_paged(q, kc, vc, table, ln)
-    again = fa.attention_decode_paged(q, kc, vc, table, ln)
+    ref = fa.attention_decode_paged(q, kc, vc, table, ln, max_seqlen_k=20000)
+    again = fa.attention_decode_paged(q, kc, vc, table, ln, max_seqlen_k=20000)
     assert torch.equal(ref[0], again[0]) and torch.equal(ref[1], again[1])
-    ws = torch.empty(fa.fa_decode_paged_workspace_bytes(3, 1, 8, 2, table.shape[1] * 64, 128), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(fa.fa_decode_paged_workspace_bytes(3, 1, 8, 2, 20000, 128), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
     ws.fill_(255)
     graphs, outs, q2 = [], [], -q
     for x in (q, q2):  # two graphs that share a workspace, replayed in turn
         graphs.append(torch.cuda.CUDAGraph())
         with torch.cuda.graph(graphs[-1]):
-            outs.append(fa.attention_decode_paged(x, kc, vc, table, ln, workspace=ws))
+            outs.append(fa.attention_decode_paged(x, kc, vc, table, ln, max_seqlen_k=20000, workspace=ws))
     for _ in range(2):
         for gr in graphs:
             gr.replay()
-    want = fa.attention_decode_paged(q2, kc, vc, table, ln)
+    want = fa.attention_decode_paged(q2, kc, vc, table, ln, max_seqlen_k=20000)
     torch.cuda.synchronize()
     assert torch.equal(outs[0][0], ref[0]) and torch.equal(outs[1][0], want[0]) and torch.equal(outs[1][1], want[1])
     sides = [torch.cuda.Stream() for _ in range(2)]  # two calls at once, each with memory of its own
-    got = [fa.attention_decode_paged(x, kc, vc, table, ln, stream=s.cuda_stream) for x, s in zip((q, q2), sides)]
+    got = [fa.attention_decode_paged(x, kc, vc, table, ln, max_seqlen_k=20000, stream=s.cuda_stream) for x, s in zip((q, q2), sides)]
     torch.cuda.synchronize()
     assert torch.equal(got[0][0], ref[0]) and torch.equal(got[1][0], want[0])
     assert _status(fa) == fa.FA_OK

@@ -114,11 +114,11 @@ def test_sizes(fa):
     assert fa.fa_decode_paged_workspace_bytes(1, 1, 4, 3, 64, 64) == 0
     assert fa.fa_decode_paged_workspace_bytes(1, 1, 4, 2, 0, 64) == 0
     # two parts of each block at most, whatever the length; small calls need none
-    for nk in (1, 100, 4096):
+    for nk in (1, 100, 8192):
         assert fa.fa_decode_paged_workspace_bytes(1, 1, 8, 8, nk, 128) == 0
-    for nk in (4097, 5000, 131072, 1 << 30):
+    for nk in (8193, 10000, 131072, 1 << 30):
         assert 0 < fa.fa_decode_paged_workspace_bytes(1, 1, 8, 8, nk, 128) < 1 << 25
-    assert fa.fa_decode_paged_workspace_bytes(64, 1, 8, 8, 2048, 128) > 0
+    assert fa.fa_decode_paged_workspace_bytes(64, 1, 8, 8, 2049, 128) > 0
 
 
 def test_wrapper_refusals(fa):
