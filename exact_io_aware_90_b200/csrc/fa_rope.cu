@@ -2,7 +2,7 @@
 // position in one pass, its gradient, and the table of angles (see rope.cuh for the row arithmetic).
 //
 // Streams of a few fp32 operations per value read and written, bound by HBM bandwidth where there are many tokens
-// (32768 tokens of 16 + 16 heads, d = 128, bf16: forward 541 MB in 91 us, gradient 810 MB in 131 us, 91 and 94 % of the
+// (32768 tokens of 16 + 16 heads, d = 128, bf16: forward 541 MB in 91 us, gradient 810 MB in 130 us, 91 and 95 % of the
 // measured copy bandwidth) and by the launch where there are few.
 //
 //   fa_qk_norm_rope_kernel      a warp takes one token: its cos and sin are loaded once and serve every
@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) fa_qk_norm_rope_bwd_kernel(co
   constexpr int G = D / 16, RPW = 32 / G, WARPS = kRopeThreads / 32;
   extern __shared__ __align__(16) uint4 s_ring[];  // [warps][stages][4 pieces][lanes]
   __shared__ float s_dw[WARPS][D];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sum of dw waits for the end of this kernel itself
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool isk = (int)blockIdx.x >= a.q_blocks;  // the first q_blocks blocks take the queries
   const int blk = isk ? blockIdx.x - a.q_blocks : blockIdx.x, nblk = isk ? gridDim.x - a.q_blocks : a.q_blocks;
@@ -129,9 +130,13 @@ __global__ void __launch_bounds__(kRopeThreads, 2) fa_qk_norm_rope_bwd_kernel(co
   // Each lane copies the pieces of its own rows ahead into its own places of the ring, so that no other thread is waited
   // for: the copies in flight, 2 KB a group, do not take registers.
   uint4* mine = s_ring + warp * (kRopeStages * 4 * 32) + lane;
-  int t = blk * WARPS + warp, h0 = 0, t_next = t, h_next = 0, stage = 0, stage_next = 0;
+  // Fewer heads than the warp has rows: it takes several tokens at a time, HP rows each (12527 tokens of 2 + 1 heads, d = 128:
+  // 10.4 us against 22.6 with one token at a time).  t: this lane's token.
+  const int HP = H >= RPW ? RPW : H > 4 ? 8 : H > 2 ? 4 : H, first = lane / G / HP, hl = lane / G % HP;
+  const int step = nblk * WARPS * (RPW / HP);
+  int t = (blk * WARPS + warp) * (RPW / HP) + first, h0 = 0, t_next = t, h_next = 0, stage = 0, stage_next = 0;
   auto issue = [&]() {
-    const int h = h_next + lane / G;
+    const int h = h_next + hl;
     if (t_next < a.T && h < H) {
       const uint32_t to = smem_u32(mine + stage_next * 128);
       const uint8_t* p = gy + ((size_t)t_next * gs + (size_t)h * D) * 2;
@@ -145,39 +150,38 @@ __global__ void __launch_bounds__(kRopeThreads, 2) fa_qk_norm_rope_bwd_kernel(co
     }
     cp_async_commit();
     stage_next = stage_next + 1 == kRopeStages ? 0 : stage_next + 1;
-    h_next += RPW;
+    h_next += HP;
     if (h_next >= H) {
       h_next = 0;
-      t_next += nblk * WARPS;
+      t_next += step;
     }
   };
 #pragma unroll
   for (int s = 0; s < kRopeStages - 1; ++s) issue();
-  float cs[8], sn[8];
-  bool ok = true;
+  float cs[8] = {}, sn[8] = {};
+  bool ok = false;
   int2 pos = t < a.T ? rope_positions(ra, t, a.T, 0, rl) : make_int2(0, 0);
 #pragma unroll 1
-  while (t < a.T) {
-    if (h0 == 0) ok = rope_angles(ra, pos, rl, cs, sn);
-    const int t_now = t, h = h0 + lane / G;
-    h0 += RPW;
+  while (t - first < a.T) {
+    if (h0 == 0) ok = rope_angles_each(ra, pos, rl, cs, sn, t < a.T, HP * G);
+    const int t_now = t, h = h0 + hl;
+    h0 += HP;
     if (h0 >= H) {
       h0 = 0;
-      t += nblk * WARPS;
+      t += step;
       if (t < a.T) pos = rope_positions(ra, t, a.T, 0, rl);
     }
     cp_async_wait<kRopeStages - 2>();
     const uint4* from = mine + stage * 128;
     stage = stage + 1 == kRopeStages ? 0 : stage + 1;
     float g[16], x[16];
-    const bool on = h < H;
+    const bool on = h < H && ok;  // a position out of range: the token is left out
     const uint4 none = make_uint4(0, 0, 0, 0);
     unpack8<BF16>(on ? from[0] : none, g);
     unpack8<BF16>(on ? from[32] : none, g + 8);
     unpack8<BF16>(on && wp != nullptr ? from[64] : none, x);
     unpack8<BF16>(on && wp != nullptr ? from[96] : none, x + 8);
     issue();  // into the place that the last turn read
-    if (!ok) continue;  // a position out of range: the token is left out
     if (rl.rot) rope_rotate<INTER, true>(g, cs, sn);
     if (wp != nullptr) {
       const float r = row_rms_inv<D>(x, a.eps);
@@ -267,13 +271,19 @@ cudaError_t launch_qk_norm_rope(const QkArgs& a, const RopeArgs& ra, int d, bool
   return bf16 ? launch_qk_t<64, true>(a, ra, stream) : launch_qk_t<64, false>(a, ra, stream);
 }
 
-// One wave of blocks (two per SM), shared between the queries and the keys by their heads; a warp per token at least.
+// One wave of blocks (two per SM), shared between the queries and the keys by the row groups of a token, of which a small
+// number of heads fills a part; a warp per group at least.
 template <int D, bool BF16>
 static cudaError_t launch_qk_bwd_t(QkBwdArgs a, const RopeArgs& ra, cudaStream_t stream) {
-  const int most = max(1, (a.T + kRopeThreads / 32 - 1) / (kRopeThreads / 32));
-  const int share = (int)((long long)kQkBwdBlocks * a.Hq / (a.Hq + a.Hk));
-  a.q_blocks = min(most, max(1, min(kQkBwdBlocks - 1, share)));
-  const int k_blocks = min(most, kQkBwdBlocks - max(1, min(kQkBwdBlocks - 1, share)));
+  constexpr int RPW = 512 / D, WARPS = kRopeThreads / 32;
+  auto rows = [](int H) { return H >= RPW ? (H + RPW - 1) / RPW * RPW : H > 4 ? 8 : H > 2 ? 4 : H; };
+  auto most = [&](int H) {
+    const int tokens = H >= RPW ? WARPS : WARPS * RPW / rows(H);  // of a block
+    return max(1, (a.T + tokens - 1) / tokens);
+  };
+  const int share = max(1, min(kQkBwdBlocks - 1, (int)((long long)kQkBwdBlocks * rows(a.Hq) / (rows(a.Hq) + rows(a.Hk)))));
+  a.q_blocks = min(most(a.Hq), share);
+  const int k_blocks = min(most(a.Hk), kQkBwdBlocks - share);
   auto kernel = ra.interleaved ? fa_qk_norm_rope_bwd_kernel<D, BF16, true> : fa_qk_norm_rope_bwd_kernel<D, BF16, false>;
   static std::atomic<unsigned long long> done[2] = {{0}, {0}};
   cudaError_t e = set_smem_once(done[ra.interleaved], reinterpret_cast<const void*>(kernel), kRopeRing);

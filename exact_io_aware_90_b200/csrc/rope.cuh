@@ -53,6 +53,18 @@ __device__ __forceinline__ int2 rope_positions(const RopeArgs& ra, int t, int T,
   return make_int2(first, axis[1] == axis[0] ? first : __ldg(ra.positions + (size_t)axis[1] * T + t));
 }
 
+// cos and sin of this lane's eight frequencies at positions that are in the table.
+__device__ __forceinline__ void rope_load(const RopeArgs& ra, int2 pos, const RopeLane& rl, float (&cs)[8], float (&sn)[8]) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const size_t at = (size_t)(u ? pos.y : pos.x) * (ra.rot_dim / 2) + rl.f0 + 4 * u;
+    const float4 c = __ldg(reinterpret_cast<const float4*>(ra.cos_t + at));
+    const float4 s = __ldg(reinterpret_cast<const float4*>(ra.sin_t + at));
+    cs[4 * u] = c.x; cs[4 * u + 1] = c.y; cs[4 * u + 2] = c.z; cs[4 * u + 3] = c.w;
+    sn[4 * u] = s.x; sn[4 * u + 1] = s.y; sn[4 * u + 2] = s.z; sn[4 * u + 3] = s.w;
+  }
+}
+
 // cos and sin of this lane's eight frequencies.  False, with the status recorded, when a position that the warp's lanes
 // read with is outside the table.
 __device__ __forceinline__ bool rope_angles(const RopeArgs& ra, int2 pos, const RopeLane& rl, float (&cs)[8], float (&sn)[8]) {
@@ -62,17 +74,22 @@ __device__ __forceinline__ bool rope_angles(const RopeArgs& ra, int2 pos, const 
     if (lane_id() == 0) record_status(1);
     return false;
   }
-  if (rl.rot) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const size_t at = (size_t)(u ? pos.y : pos.x) * (ra.rot_dim / 2) + rl.f0 + 4 * u;
-      const float4 c = __ldg(reinterpret_cast<const float4*>(ra.cos_t + at));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(ra.sin_t + at));
-      cs[4 * u] = c.x; cs[4 * u + 1] = c.y; cs[4 * u + 2] = c.z; cs[4 * u + 3] = c.w;
-      sn[4 * u] = s.x; sn[4 * u + 1] = s.y; sn[4 * u + 2] = s.z; sn[4 * u + 3] = s.w;
-    }
-  }
+  if (rl.rot) rope_load(ra, pos, rl, cs, sn);
   return true;
+}
+
+// The same where the warp has several tokens, `width` lanes each (a power of two): a bad position leaves out its token alone,
+// and leaves cos and sin as they were.  Lanes without a token (`on` false) ask for nothing.
+__device__ __forceinline__ bool rope_angles_each(const RopeArgs& ra, int2 pos, const RopeLane& rl, float (&cs)[8], float (&sn)[8], bool on,
+                                                 int width) {
+  const bool bad = on && rl.rot && ((unsigned)pos.x >= (unsigned)ra.table_rows || (unsigned)pos.y >= (unsigned)ra.table_rows);
+  const uint32_t votes = __ballot_sync(0xffffffffu, bad), lanes = 0xffffffffu >> (32 - width) << (lane_id() & ~(uint32_t)(width - 1));
+  if ((votes & lanes) != 0u) {
+    if ((lane_id() & (uint32_t)(width - 1)) == 0u) record_status(1);
+    return false;
+  }
+  if (on && rl.rot) rope_load(ra, pos, rl, cs, sn);
+  return on;
 }
 
 template <bool BF16>

@@ -66,6 +66,8 @@ SHAPES = [  # T, hq, hk, d, rot, interleaved, axes
     (1, 1, 1, 64, 64, False, 1), (1, 5, 1, 128, 128, False, 1), (2, 4, 2, 64, 16, True, 1), (7, 3, 3, 128, 48, False, 2),
     (8, 16, 16, 128, 128, False, 1), (9, 17, 2, 64, 64, False, 3), (33, 8, 8, 128, 96, True, 3), (301, 12, 4, 64, 48, True, 4),
     (129, 1, 9, 128, 16, False, 1), (2500, 4, 4, 128, 128, False, 1),
+    # few heads: several tokens in a warp, the last warp not full
+    (301, 2, 1, 64, 32, False, 1), (5, 3, 2, 64, 64, True, 1), (6001, 1, 2, 128, 128, False, 1), (4003, 12, 1, 64, 64, True, 3),
 ]
 
 
@@ -179,10 +181,13 @@ def test_positions_out_of_range_are_skipped(fa, bad):
     assert torch.equal(oq, yq) and torch.equal(ok, yk)
     # the gradient of a skipped token adds nothing to dw
     zq, zk = x["gq"].clone(), x["gk"].clone()
-    _, _, dwq, dwk = fa.attention_qk_norm_rope_backward(zq, zk, *args, pos, q=q, k=k, wq=x["wq"], wk=x["wk"])
+    dq, dk = torch.full_like(zq, 3.0), torch.full_like(zk, 3.0)
+    _, _, dwq, dwk = fa.attention_qk_norm_rope_backward(zq, zk, *args, pos, q=q, k=k, wq=x["wq"], wk=x["wk"], dq=dq, dk=dk)
     assert _status(fa) == fa.FA_ERR_INVALID_ARG
     zq[11], zk[11] = 0.0, 0.0
-    _, _, ewq, ewk = fa.attention_qk_norm_rope_backward(zq, zk, *args, x["pos"], q=q, k=k, wq=x["wq"], wk=x["wk"])
+    eq, ek, ewq, ewk = fa.attention_qk_norm_rope_backward(zq, zk, *args, x["pos"], q=q, k=k, wq=x["wq"], wk=x["wk"])
+    eq[11], ek[11] = 3.0, 3.0  # nor is it written; the others are
+    assert torch.equal(dq, eq) and torch.equal(dk, ek)
     assert torch.equal(dwq, ewq) and torch.equal(dwk, ewk) and _status(fa) == fa.FA_OK
 
 
