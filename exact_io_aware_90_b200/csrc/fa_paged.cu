@@ -1168,7 +1168,8 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p
   finish_row<D, BF16>(p, paged_row(p, note.x, hk, row), lane, M, ell, acc);
 }
 
-// Row tiles of a key head, and the rows of one.
+// Row tiles of a key head, and the rows of one (32, which d = 64 has registers for, were no faster: 27 x 8192 keys of 60 rows
+// 41.2 us against 39.5).
 static int paged_tile_rows(int R) { return R <= 8 ? 8 : 16; }
 
 // Blocks that can take a run: all that fit the GPU at once (at most four per SM), or one per granule of the longest batch.

@@ -132,9 +132,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) fa_qk_norm_rope_bwd_kernel(co
   uint4* mine = s_ring + warp * (kRopeStages * 4 * 32) + lane;
   // Fewer heads than the warp has rows: it takes several tokens at a time, HP rows each (12527 tokens of 2 + 1 heads, d = 128:
   // 10.4 us against 22.6 with one token at a time).  t: this lane's token.
-  const int HP = H >= RPW ? RPW : H > 4 ? 8 : H > 2 ? 4 : H, first = lane / G / HP, hl = lane / G % HP;
-  const int step = nblk * WARPS * (RPW / HP);
-  int t = (blk * WARPS + warp) * (RPW / HP) + first, h0 = 0, t_next = t, h_next = 0, stage = 0, stage_next = 0;
+  const int bits = H >= RPW ? (D == 64 ? 3 : 2) : H > 4 ? 3 : H > 2 ? 2 : H - 1, HP = 1 << bits;
+  const int first = lane / G >> bits, hl = lane / G & (HP - 1);
+  const int step = nblk * WARPS * (RPW >> bits);
+  int t = (blk * WARPS + warp) * (RPW >> bits) + first, h0 = 0, t_next = t, h_next = 0, stage = 0, stage_next = 0;
   auto issue = [&]() {
     const int h = h_next + hl;
     if (t_next < a.T && h < H) {
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) fa_qk_norm_rope_bwd_kernel(co
   int2 pos = t < a.T ? rope_positions(ra, t, a.T, 0, rl) : make_int2(0, 0);
 #pragma unroll 1
   while (t - first < a.T) {
-    if (h0 == 0) ok = rope_angles_each(ra, pos, rl, cs, sn, t < a.T, HP * G);
+    if (h0 == 0) ok = rope_angles_each(ra, pos, rl, cs, sn, t < a.T, G << bits);
     const int t_now = t, h = h0 + hl;
     h0 += HP;
     if (h0 >= H) {
