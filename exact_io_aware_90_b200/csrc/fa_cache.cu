@@ -30,7 +30,7 @@ __device__ __forceinline__ bool owner_of(const int32_t* cu, int B, int T, int t,
   }
   b = find_sequence(cu, B, t);
   if (b >= B) return false;
-  const int first = __ldg(cu + b), end = __ldg(cu + b + 1);
+  const int first = load_now(cu + b), end = load_now(cu + b + 1);
   if (t < first) return false;  // before the first sequence
   if (first < 0 || end > T || t >= end) {
     if (lane_id() == 0) record_status(1);
@@ -80,6 +80,7 @@ __device__ __forceinline__ void store_q4(uint4* rows, const RopeLane& rl, int la
 template <int D, bool BF16, bool INTER, bool Q4, int U>
 __global__ void __launch_bounds__(kCacheThreads, U == 2 ? 3 : 2) fa_cache_append_kernel(const AppendArgs a, const RopeArgs ra, const PagedArgs pg) {
   constexpr int G = D / 16, RPW = 32 / G;
+  after_earlier_kernels();
   __shared__ uint4 s_rows[Q4 ? kCacheThreads / 32 : 1][Q4 ? 64 : 1];  // a warp's rows, 512 values
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * (kCacheThreads / 32) + warp;
@@ -98,8 +99,8 @@ __global__ void __launch_bounds__(kCacheThreads, U == 2 ? 3 : 2) fa_cache_append
     for (int u = 0; u < U; ++u) {
       v0[u] = v1[u] = make_uint4(0, 0, 0, 0);
       if (h + u * RPW < H) {
-        v0[u] = __ldcs(reinterpret_cast<const uint4*>(src + u * RPW * D * 2 + c0));
-        v1[u] = __ldcs(reinterpret_cast<const uint4*>(src + u * RPW * D * 2 + c1));
+        v0[u] = load_once(reinterpret_cast<const uint4*>(src + u * RPW * D * 2 + c0));
+        v1[u] = load_once(reinterpret_cast<const uint4*>(src + u * RPW * D * 2 + c1));
       }
     }
     src += (size_t)gridDim.y * (RPW * U * D * 2);
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(kCacheThreads, U == 2 ? 3 : 2) fa_cache_append
 
   int b, i, n;
   if (!owner_of(a.cu_seqlens, pg.B, a.T, t, b, i, n)) return;
-  const int len = __ldg(pg.seqlens_k + b);
+  const int len = load_now(pg.seqlens_k + b);
   const int at = len - n + i;
   const int2 pos = rope_positions(ra, t, a.T, at, rl);
   int slot;
@@ -127,8 +128,8 @@ __global__ void __launch_bounds__(kCacheThreads, U == 2 ? 3 : 2) fa_cache_append
     const void* wp = part == 0 ? a.wq : a.wk;
     uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
     if (wp != nullptr) {
-      w0 = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + c0));
-      w1 = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + c1));
+      w0 = load_now(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + c0));
+      w1 = load_now(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + c1));
     }
     const size_t block = cache_block_bytes(D, pg.page_size, Q4);
     uint8_t* dst = part == 0 ? static_cast<uint8_t*>(a.q_out) + (t * a.q_out_stride + (long long)h_first * D) * 2
@@ -211,12 +212,13 @@ __device__ __forceinline__ float2 pair_of(uint32_t pair) { return __half22float2
 template <int D, bool BF16, bool Q4, int U>
 __global__ void __launch_bounds__(kCacheThreads) fa_cache_gather_kernel(const GatherArgs a, const PagedArgs pg) {
   constexpr int G = D / 16, RPW = 32 / G, W = D / 32;
+  after_earlier_kernels();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G;
   const int t = blockIdx.x * (kCacheThreads / 32) + warp;
   if (t >= a.T) return;
   int b, i, n;
   if (!owner_of(a.cu_seqlens, pg.B, a.T, t, b, i, n)) return;
-  const int start = a.starts != nullptr ? __ldg(a.starts + b) : 0;
+  const int start = a.starts != nullptr ? load_now(a.starts + b) : 0;
   int slot;
   const int page = page_of(pg, b, start < 0 || start > 0x7fffffff - i ? -1 : start + i, slot);
   if (page < 0) return;
@@ -237,10 +239,10 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_gather_kernel(const Ga
         if (h + u * RPW < pg.Hk) {
           const uint4* pk = reinterpret_cast<const uint4*>(kb + (off + u * RPW) * block + row);
           const uint4* pv = reinterpret_cast<const uint4*>(vb + (off + u * RPW) * block + row);
-          x[u][0] = __ldcs(pk + l);
-          x[u][1] = __ldcs(pk + G + l);
-          x[u][2] = __ldcs(pv + l);
-          x[u][3] = __ldcs(pv + G + l);
+          x[u][0] = load_once(pk + l);
+          x[u][1] = load_once(pk + G + l);
+          x[u][2] = load_once(pv + l);
+          x[u][3] = load_once(pv + G + l);
         }
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -263,14 +265,14 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_gather_kernel(const Ga
         if (h + u * RPW < pg.Hk) {
           const uint8_t* pk = kb + (off + u * RPW) * block;
           const uint8_t* pv = vb + (off + u * RPW) * block;
-          kn[u] = __ldcs(reinterpret_cast<const uint2*>(pk + row) + l);
-          vn[u] = __ldcs(reinterpret_cast<const uint2*>(pv + row) + l);
-          kp[u] = __ldg(reinterpret_cast<const uint2*>(pk + pairs + 4 * w2));
+          kn[u] = load_once(reinterpret_cast<const uint2*>(pk + row) + l);
+          vn[u] = load_once(reinterpret_cast<const uint2*>(pv + row) + l);
+          kp[u] = load_now(reinterpret_cast<const uint2*>(pk + pairs + 4 * w2));
           if constexpr (W == 4) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(pv + pairs));
+            const uint4 v = load_now(reinterpret_cast<const uint4*>(pv + pairs));
             vp[u][0] = v.x; vp[u][1] = v.y; vp[u][2] = v.z; vp[u][3] = v.w;
           } else {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(pv + pairs));
+            const uint2 v = load_now(reinterpret_cast<const uint2*>(pv + pairs));
             vp[u][0] = v.x; vp[u][1] = v.y;
           }
         }
@@ -308,9 +310,8 @@ static cudaError_t launch_append_u(const AppendArgs& a, const RopeArgs& ra, cons
   constexpr int ROWS = 512 / D * U;
   dim3 grid = cache_grid(a.T, (max(a.Hq, pg.Hk) + ROWS - 1) / ROWS);
   if (U == 1) grid.z = 3;
-  if (ra.interleaved) fa_cache_append_kernel<D, BF16, true, Q4, U><<<grid, kCacheThreads, 0, stream>>>(a, ra, pg);
-  else fa_cache_append_kernel<D, BF16, false, Q4, U><<<grid, kCacheThreads, 0, stream>>>(a, ra, pg);
-  return cudaPeekAtLastError();
+  return launch_after(ra.interleaved ? fa_cache_append_kernel<D, BF16, true, Q4, U> : fa_cache_append_kernel<D, BF16, false, Q4, U>, grid,
+                      dim3(kCacheThreads), 0, stream, a, ra, pg);
 }
 
 // Two row groups together where the tokens fill the GPU; else one, with the heads, and queries, keys and values, spread
@@ -332,13 +333,8 @@ static cudaError_t launch_gather_t(const GatherArgs& a, const PagedArgs& pg, cud
   constexpr int RPW = 512 / D;
   const bool many = a.T >= 2 * kSmCount * (kCacheThreads / 32) && pg.Hk > RPW;
   const dim3 grid = cache_grid(a.T, (pg.Hk + RPW - 1) / RPW);
-  if (pg.q4) {
-    if (many) fa_cache_gather_kernel<D, BF16, true, 2><<<grid, kCacheThreads, 0, stream>>>(a, pg);
-    else fa_cache_gather_kernel<D, BF16, true, 1><<<grid, kCacheThreads, 0, stream>>>(a, pg);
-  } else {
-    fa_cache_gather_kernel<D, BF16, false, 1><<<grid, kCacheThreads, 0, stream>>>(a, pg);
-  }
-  return cudaPeekAtLastError();
+  auto kernel = !pg.q4 ? fa_cache_gather_kernel<D, BF16, false, 1> : many ? fa_cache_gather_kernel<D, BF16, true, 2> : fa_cache_gather_kernel<D, BF16, true, 1>;
+  return launch_after(kernel, grid, dim3(kCacheThreads), 0, stream, a, pg);
 }
 
 cudaError_t launch_cache_gather(const GatherArgs& a, const PagedArgs& pg, cudaStream_t stream) {

@@ -30,7 +30,7 @@
 //
 // Measured, d = 128: 16 x 8192 keys of 16 heads in 16 bits 1074 MB in 164 us (100 % of the measured copy bandwidth);
 // 64 sequences of 512 to 16384 keys, 8 key heads, 4 query heads each, in 4 bits 743 MB in 162 us (70 %); 131071 keys of 8
-// heads, 16 query rows, fp16, in 4 bits 168 MB in 70 us (37 %); one sequence of 777 keys and 16 heads 6.8 us (the launch and
+// heads, 16 query rows, fp16, in 4 bits 168 MB in 70 us (37 %); one sequence of 777 keys and 16 heads 6.1 us (the launch and
 // a chain of lookups and copies).
 //
 // The reference of the exponents rises only when a score passes it by 2^8 (one vote per tile).  P of 16-bit caches is
@@ -141,7 +141,7 @@ __device__ __forceinline__ uint32_t less8(uint32_t x) {
 
 // The sequence's key count, or -1 when it is out of range.
 __device__ __forceinline__ int paged_length(const PagedParams& p, int b) {
-  const int L = __ldg(p.pg.seqlens_k + b);
+  const int L = load_now(p.pg.seqlens_k + b);
   return L < 0 || L > p.most ? -1 : L;
 }
 
@@ -359,7 +359,7 @@ struct Rows16 {
       const uint8_t* src = p.q + (on ? paged_row(p, b, hk, r) : 0) * D * 2;
 #pragma unroll
       for (int j = 0; j < W; ++j) {
-        const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(src + (32 * j + 8 * t) * 2)) : make_uint4(0, 0, 0, 0);
+        const uint4 v = on ? load_now(reinterpret_cast<const uint4*>(src + (32 * j + 8 * t) * 2)) : make_uint4(0, 0, 0, 0);
         qb[nt][2 * j][0] = v.x;
         qb[nt][2 * j][1] = v.y;
         qb[nt][2 * j + 1][0] = v.z;
@@ -561,7 +561,7 @@ struct Rows4 {
       float f[W][8], most = 0.f;
 #pragma unroll
       for (int j = 0; j < W; ++j) {
-        const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(src + (32 * j + 8 * t) * 2)) : make_uint4(0, 0, 0, 0);
+        const uint4 v = on ? load_now(reinterpret_cast<const uint4*>(src + (32 * j + 8 * t) * 2)) : make_uint4(0, 0, 0, 0);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -883,9 +883,9 @@ __device__ __forceinline__ void run_piece(const PagedParams& p, uint8_t* smem, i
       const TileCopy<D, Q4> copy(p.pg, hk, ring, lane);
       int next_j = GK * first + T * warp;  // the first key of the next tile to be copied
       int page_i = next_j / ps, slot = next_j - page_i * ps;
-      int page = tiles > 0 ? __ldg(table + page_i) : 0, page2 = 0;
+      int page = tiles > 0 ? load_now(table + page_i) : 0, page2 = 0;
       auto second = [&]() { return slot + 16 >= ps ? page_i + 1 : page_i; };  // the second half's page index
-      if (paired && tiles > 0 && next_j + 16 < L) page2 = __ldg(table + second());
+      if (paired && tiles > 0 && next_j + 16 < L) page2 = load_now(table + second());
       int left = tiles;      // to be copied
       uint32_t copy_at = 0;  // the stage of the next one
       uint32_t valid = 0;    // two bits for each of the last tiles copied: the halves that are there
@@ -917,8 +917,8 @@ __device__ __forceinline__ void run_piece(const PagedParams& p, uint8_t* smem, i
             ++page_i;
           }
           if (left > 0) {
-            page = __ldg(table + page_i);
-            if (paired && next_j + 16 < L) page2 = __ldg(table + second());
+            page = load_now(table + page_i);
+            if (paired && next_j + 16 < L) page2 = load_now(table + second());
           }
         }
         copy_at = copy_at == (S - 1) * Cfg::kTileBytes ? 0 : copy_at + Cfg::kTileBytes;
@@ -995,7 +995,8 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
   const int lane = threadIdx.x & 31;
   const int units = p.pg.Hk * p.tiles;  // of one sequence
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // for the merge
+  after_earlier_kernels();
 
   // ---- this block's run of granules
   const GranuleScan scan = scan_granules(p);
@@ -1083,6 +1084,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedConfig<D, Q4, NT>::kBlock
   constexpr int W = D / 32, ROWS = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_ml[ROWS][2];
+  after_earlier_kernels();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -1135,14 +1137,14 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p
   constexpr int F = D / 32;
   __shared__ float s_o[4][D], s_l[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y, tile_rows = gridDim.y;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 note = __ldcg(p.units + blockIdx.x);  // sequence, unit of it, first worker, parts
+  after_earlier_kernels();
+  const int4 note = load_now(p.units + blockIdx.x);  // sequence, unit of it, first worker, parts
   const int hk = note.y % p.pg.Hk, row = note.y / p.pg.Hk * tile_rows + r, w0 = note.z, parts = note.w;
   if (parts == 0 || row >= p.R) return;
   // the first worker's part is its last one (slot 1), the others' their first (slot 0)
   auto slot = [&](int i) { return (size_t)(2 * (w0 + i) + (i == 0 ? 1 : 0)) * tile_rows + r; };
   float M = -INFINITY;
-  for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(p.part_ml + 2 * slot(i)));
+  for (int i = lane; i < parts; i += 32) M = fmaxf(M, load_now(p.part_ml + 2 * slot(i)));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   float ell = 0.f, acc[F];
@@ -1151,11 +1153,11 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p
 #pragma unroll 4
   for (int i = warp; i < parts; i += 4) {
     const size_t s = slot(i);
-    const float a = join_weight(__ldcg(p.part_ml + 2 * s), M);
-    ell = fmaf(__ldcg(p.part_ml + 2 * s + 1), a, ell);
+    const float a = join_weight(load_now(p.part_ml + 2 * s), M);
+    ell = fmaf(load_now(p.part_ml + 2 * s + 1), a, ell);
     const float* src = p.part_o + s * D;
 #pragma unroll
-    for (int j = 0; j < F; ++j) acc[j] = fmaf(__ldcg(src + 32 * j + lane), a, acc[j]);
+    for (int j = 0; j < F; ++j) acc[j] = fmaf(load_now(src + 32 * j + lane), a, acc[j]);
   }
 #pragma unroll
   for (int j = 0; j < F; ++j) s_o[warp][32 * j + lane] = acc[j];
@@ -1224,22 +1226,23 @@ static cudaError_t launch_paged_v(PagedParams p, int B, int Nk, cudaStream_t str
     cfg.blockDim = dim3(kPagedThreads);
     cfg.dynamicSmemBytes = Cfg::kSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)C;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, fa_paged_cluster_kernel<D, BF16, Q4, NT>, p);
   }
   p.workers = paged_workers(B, p.pg.Hk, p.tiles, Nk, Cfg::kGranule, Cfg::kBlocks);
   p.by_unit = (long long)B * p.pg.Hk * p.tiles <= p.workers;
-  fa_paged_split_kernel<D, BF16, Q4, NT><<<p.workers, kPagedThreads, Cfg::kSmem, stream>>>(p);
-  e = cudaPeekAtLastError();
+  e = launch_after(fa_paged_split_kernel<D, BF16, Q4, NT>, dim3((unsigned)p.workers), dim3(kPagedThreads), Cfg::kSmem, stream, p);
   if (e != cudaSuccess) return e;
   // the merge is launched while the runs end; it waits for them before it reads
   const unsigned notes = (unsigned)(p.by_unit ? B * p.pg.Hk * p.tiles : p.workers);
-  return launch_after(fa_paged_merge_kernel<D, BF16>, dim3(notes, 8 * NT), dim3(128), stream, p);
+  return launch_after(fa_paged_merge_kernel<D, BF16>, dim3(notes, 8 * NT), dim3(128), 0, stream, p);
 }
 
 template <int D, bool BF16>

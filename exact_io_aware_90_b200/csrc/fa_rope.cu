@@ -40,14 +40,15 @@ __global__ void __launch_bounds__(256) fa_rope_table_kernel(float* cos_t, float*
 template <int D, bool BF16>
 __device__ __forceinline__ void load_weights(const void* w, const RopeLane& rl, float (&x)[16]) {
   const uint8_t* p = static_cast<const uint8_t*>(w);
-  unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(p + 2 * rl.c0)), x);
-  unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(p + 2 * rl.c1)), x + 8);
+  unpack8<BF16>(load_now(reinterpret_cast<const uint4*>(p + 2 * rl.c0)), x);
+  unpack8<BF16>(load_now(reinterpret_cast<const uint4*>(p + 2 * rl.c1)), x + 8);
 }
 
 // U: row groups (of 512/d rows) that a warp loads before it works on the first.
 template <int D, bool BF16, bool INTER, int U>
 __global__ void __launch_bounds__(kRopeThreads, 3) fa_qk_norm_rope_kernel(const QkArgs a, const RopeArgs ra) {
   constexpr int G = D / 16, RPW = 32 / G;  // lanes per row, rows per warp at a time
+  after_earlier_kernels();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * (kRopeThreads / 32) + warp;
   if (t >= a.T) return;
@@ -62,8 +63,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) fa_qk_norm_rope_kernel(const 
     const void* wp = part == 0 ? a.wq : a.wk;
     uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;  // the weights stay packed: unpacking costs less than the registers
     if (wp != nullptr) {
-      w0 = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + 2 * rl.c0));
-      w1 = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + 2 * rl.c1));
+      w0 = load_now(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + 2 * rl.c0));
+      w1 = load_now(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + 2 * rl.c1));
     }
 #pragma unroll 1
     for (int h0 = blockIdx.y * (RPW * U); h0 < H; h0 += gridDim.y * (RPW * U)) {
@@ -74,8 +75,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) fa_qk_norm_rope_kernel(const 
         v0[u] = v1[u] = make_uint4(0, 0, 0, 0);
         if (h + u * RPW < H) {
           const uint8_t* p = src + (size_t)(h + u * RPW) * D * 2;
-          v0[u] = __ldcs(reinterpret_cast<const uint4*>(p + 2 * rl.c0));
-          v1[u] = __ldcs(reinterpret_cast<const uint4*>(p + 2 * rl.c1));
+          v0[u] = load_once(reinterpret_cast<const uint4*>(p + 2 * rl.c0));
+          v1[u] = load_once(reinterpret_cast<const uint4*>(p + 2 * rl.c1));
         }
       }
 #pragma unroll
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) fa_qk_norm_rope_bwd_kernel(co
   constexpr int G = D / 16, RPW = 32 / G, WARPS = kRopeThreads / 32;
   extern __shared__ __align__(16) uint4 s_ring[];  // [warps][stages][4 pieces][lanes]
   __shared__ float s_dw[WARPS][D];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sum of dw waits for the end of this kernel itself
+  after_earlier_kernels();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool isk = (int)blockIdx.x >= a.q_blocks;  // the first q_blocks blocks take the queries
   const int blk = isk ? blockIdx.x - a.q_blocks : blockIdx.x, nblk = isk ? gridDim.x - a.q_blocks : a.q_blocks;
@@ -121,8 +122,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) fa_qk_norm_rope_bwd_kernel(co
   const RopeLane rl = rope_lane<INTER>(lane % G, ra.rot_dim);
   uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
   if (wp != nullptr) {
-    w0 = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + 2 * rl.c0));
-    w1 = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + 2 * rl.c1));
+    w0 = load_now(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + 2 * rl.c0));
+    w1 = load_now(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(wp) + 2 * rl.c1));
   }
   float dw[16];
 #pragma unroll
@@ -235,10 +236,10 @@ __global__ void __launch_bounds__(1024) fa_qk_norm_rope_dw_kernel(const float* p
   const bool isk = blockIdx.y != 0;
   const int first = isk ? q_blocks : 0, n = isk ? k_blocks : q_blocks;
   const int f = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_earlier_kernels();
   float v = 0.f;
 #pragma unroll 4
-  for (int b = slice; b < n; b += 32) v += __ldcg(part + (size_t)(first + b) * d + f);
+  for (int b = slice; b < n; b += 32) v += load_now(part + (size_t)(first + b) * d + f);
   s[slice][threadIdx.x & 31] = v;
   __syncthreads();
   if (slice == 0) {
@@ -254,9 +255,8 @@ template <int D, bool BF16, int U>
 static cudaError_t launch_qk_u(const QkArgs& a, const RopeArgs& ra, int blocks, cudaStream_t stream) {
   const int most = (max(a.Hq, a.Hk) + 512 / D * U - 1) / (512 / D * U);
   const dim3 grid(blocks, max(1, min(most, 2 * kSmCount / blocks)));  // few tokens: the heads are spread over blocks too
-  if (ra.interleaved) fa_qk_norm_rope_kernel<D, BF16, true, U><<<grid, kRopeThreads, 0, stream>>>(a, ra);
-  else fa_qk_norm_rope_kernel<D, BF16, false, U><<<grid, kRopeThreads, 0, stream>>>(a, ra);
-  return cudaPeekAtLastError();
+  return launch_after(ra.interleaved ? fa_qk_norm_rope_kernel<D, BF16, true, U> : fa_qk_norm_rope_kernel<D, BF16, false, U>, grid,
+                      dim3(kRopeThreads), 0, stream, a, ra);
 }
 
 // Two row groups ahead where the blocks fill the GPU (32768 tokens x 32 heads, d = 128: 89.6 us against 110.7 with one
@@ -289,10 +289,9 @@ static cudaError_t launch_qk_bwd_t(QkBwdArgs a, const RopeArgs& ra, cudaStream_t
   static std::atomic<unsigned long long> done[2] = {{0}, {0}};
   cudaError_t e = set_smem_once(done[ra.interleaved], reinterpret_cast<const void*>(kernel), kRopeRing);
   if (e != cudaSuccess) return e;
-  kernel<<<a.q_blocks + k_blocks, kRopeThreads, kRopeRing, stream>>>(a, ra);
-  e = cudaPeekAtLastError();
+  e = launch_after(kernel, dim3(a.q_blocks + k_blocks), dim3(kRopeThreads), kRopeRing, stream, a, ra);
   if (e != cudaSuccess || a.wq == nullptr) return e;
-  return launch_after(fa_qk_norm_rope_dw_kernel, dim3(D / 32, 2), dim3(1024), stream, (const float*)a.part, a.dwq, a.dwk, a.q_blocks, k_blocks, D);
+  return launch_after(fa_qk_norm_rope_dw_kernel, dim3(D / 32, 2), dim3(1024), 0, stream, (const float*)a.part, a.dwq, a.dwk, a.q_blocks, k_blocks, D);
 }
 
 cudaError_t launch_qk_norm_rope_bwd(const QkBwdArgs& a, const RopeArgs& ra, int d, bool bf16, cudaStream_t stream) {

@@ -30,13 +30,13 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int B, int t) {
   while (n > 32) {
     const int step = (n + 31) / 32;
     const int i = (lane + 1) * step - 1;
-    const bool below = i < n && __ldg(cu + 1 + lo + i) <= t;
+    const bool below = i < n && load_now(cu + 1 + lo + i) <= t;
     const int c = __popc(__ballot_sync(0xffffffffu, below));
     lo += c * step;
     n = min(step, n - c * step);
     if (n <= 0) return lo;
   }
-  const bool below = lane < n && __ldg(cu + 1 + lo + lane) <= t;
+  const bool below = lane < n && load_now(cu + 1 + lo + lane) <= t;
   return lo + __popc(__ballot_sync(0xffffffffu, below));
 }
 
@@ -48,7 +48,7 @@ __device__ __forceinline__ int page_of(const PagedArgs& p, int b, int at, int& s
   if (at >= 0 && at / p.page_size < p.max_pages) {
     const int i = at / p.page_size;
     slot = at - i * p.page_size;
-    page = __ldg(p.page_table + (size_t)b * p.max_pages + i);
+    page = load_now(p.page_table + (size_t)b * p.max_pages + i);
     if (page >= p.num_pages) page = -1;
   }
   if (page < 0) {

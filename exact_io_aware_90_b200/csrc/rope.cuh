@@ -49,8 +49,8 @@ __device__ __forceinline__ int2 rope_positions(const RopeArgs& ra, int t, int T,
 #pragma unroll
       for (int a = 0; a < kRopeMaxAxes - 1; ++a) axis[u] += (a + 1 < ra.axes && rl.f0 + 4 * u >= ra.section_end[a]) ? 1 : 0;
   }
-  const int first = __ldg(ra.positions + (size_t)axis[0] * T + t);
-  return make_int2(first, axis[1] == axis[0] ? first : __ldg(ra.positions + (size_t)axis[1] * T + t));
+  const int first = load_now(ra.positions + (size_t)axis[0] * T + t);
+  return make_int2(first, axis[1] == axis[0] ? first : load_now(ra.positions + (size_t)axis[1] * T + t));
 }
 
 // cos and sin of this lane's eight frequencies at positions that are in the table.
@@ -58,8 +58,8 @@ __device__ __forceinline__ void rope_load(const RopeArgs& ra, int2 pos, const Ro
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const size_t at = (size_t)(u ? pos.y : pos.x) * (ra.rot_dim / 2) + rl.f0 + 4 * u;
-    const float4 c = __ldg(reinterpret_cast<const float4*>(ra.cos_t + at));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(ra.sin_t + at));
+    const float4 c = load_now(reinterpret_cast<const float4*>(ra.cos_t + at));
+    const float4 s = load_now(reinterpret_cast<const float4*>(ra.sin_t + at));
     cs[4 * u] = c.x; cs[4 * u + 1] = c.y; cs[4 * u + 2] = c.z; cs[4 * u + 3] = c.w;
     sn[4 * u] = s.x; sn[4 * u + 1] = s.y; sn[4 * u + 2] = s.z; sn[4 * u + 3] = s.w;
   }
