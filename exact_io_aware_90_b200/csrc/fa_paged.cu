@@ -54,7 +54,11 @@
 //     key that the minimum takes away again: over 131071 keys the tensor cores' truncating sums left 8e-4 of the
 //     output.  For one row tile −8·ΣP is a product of its own (no instruction per number); two row tiles share a
 //     subtraction per number, and so do fp16 outputs.
-//   * The reference is 2^7 below the maximum (less where scales pass 1), so that fp16's range serves P from 2^15 down.
+//   * A key's minima and scales are divided by the power of two 2^e over the largest of them and its probability is multiplied
+//     by it, and the reference is 2^7 under the largest p·2^e: fp16's range counts from the key whose values weigh most.  With
+//     the reference under the largest p alone, small values beside a key that outweighs them lost their products with the
+//     scale, and large values of no weight pushed the others out of the range (7 % of the output over 2048 keys).  Costs 30
+//     instructions per tile: 64 sequences 161 -> 167 us, 131071 keys 71.8 -> 72.6.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -240,6 +244,17 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
   uint32_t v;
   asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1 + %2];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(a), "n"(OFF));
   return v;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ void fma_pair(float& x, float& y, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\tfma.rn.f32x2 c, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, c;\n\t}" : "=f"(x), "=f"(y) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void sub_pair(float& x, float& y, float a0, float a1, float b0, float b1) {
+  fma_pair(x, y, b0, b1, -1.f, -1.f, a0, a1);
+}
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -531,12 +546,12 @@ struct Rows4 {
   static constexpr bool kCentre = NT == 1 && !kRest;  // −8·ΣP as a product
   static constexpr int NS = 2;  // sub-tiles in flight together
   static constexpr float kDepth = 7.f;      // the reference is 2^7 under the maximum
+  static constexpr float kNone = -3.4028234663852886e38f;  // the reference of a row that has met no key: under every score
   uint32_t qb[NT][KS][2], qs[NT];
-  float m[NT][2], mz[NT][2], rise_at[NT][2];
+  float m[NT][2];  // the reference of s_j + e_j
   float l[NT][2], o[NT][KS][4], mins[NT][4], coef[NT][2];
   int lim[NT][2];
   uint32_t lane_k, lane_v, lane_p, lane_m, lane_a, lane_s;
-  float cap, cap_value;  // a power of two (and its log2), at least 1, that no value scale of the warp passes
   int g, t, lane, L, Nq;
 
   __device__ __forceinline__ void init(const PagedParams& p, int b, int hk, int r0, int len, int lane_) {
@@ -545,8 +560,6 @@ struct Rows4 {
     t = lane & 3;
     L = len;
     Nq = p.Nq;
-    cap = 0.f;
-    cap_value = 1.f;
     lane_k = lane * PAIR;  // 16 (8) bytes of row g from 16t (8t) on
     lane_v = 32 * ROW + (D == 128 ? 16 * v4_piece<D>(2 * t, g >> 1) + 8 * (g & 1) : 16 * v4_piece<D>(2 * t, g >> 2) + 4 * (g & 3));
     lane_p = 64 * ROW + g * PAIR;                          // the keys' pairs of row g
@@ -605,8 +618,8 @@ struct Rows4 {
       for (int u = 0; u < 2; ++u) {
         const int rr = r0 + 8 * nt + 2 * t + u;
         lim[nt][u] = L - Nq + (rr < p.R ? rr / p.G : Nq - 1);
-        m[nt][u] = rise_at[nt][u] = -INFINITY;
-        mz[nt][u] = l[nt][u] = 0.f;
+        m[nt][u] = kNone;
+        l[nt][u] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) mins[nt][i] = 0.f;
@@ -617,6 +630,7 @@ struct Rows4 {
     }
   }
 
+  // Of s_j + e_j.
   static __device__ __forceinline__ float top_of(const float (&s)[NS][NT][4], int nt, int u) {
     float x = fmaxf(s[0][nt][u], s[0][nt][2 + u]);
 #pragma unroll
@@ -627,46 +641,22 @@ struct Rows4 {
   __device__ __forceinline__ void step(uint32_t tile, int j0, uint32_t flags) {
     const bool special = j0 + 32 > L || flags != 3u;  // some keys are not there
     auto live = [&](int sub, int key) { return ((flags >> sub) & 1u) != 0u && j0 + 16 * sub + key < L; };
-    // ---- values that are not there get minimum and scale 0 (what the tile holds of them may be anything)
-    if (special) {
-      if (!live(lane >> 4, lane & 15)) {
-        const uint32_t a = tile + 64 * ROW + 32 * PAIR + lane * PAIR;
-#pragma unroll
-        for (int j = 0; j < W; ++j) st_shared_f32(a + 4 * j, 0u);
-      }
-      __syncwarp();
+    // ---- the values' pairs of row `lane`
+    uint32_t w[W];
+    const uint32_t aw = tile + 64 * ROW + 32 * PAIR + lane * PAIR;
+    if constexpr (W == 4) {
+      const uint4 x = lds128<0>(aw);
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else {
+      const uint2 x = lds64<0>(aw);
+      w[0] = x.x; w[1] = x.y;
     }
-    // ---- the largest value scale: lane r looks at row r
-    float most;
-    {
-      uint32_t w[W];
-      const uint32_t a = tile + 64 * ROW + 32 * PAIR + lane * PAIR;
-      if constexpr (W == 4) {
-        const uint4 x = lds128<0>(a);
-        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-      } else {
-        const uint2 x = lds64<0>(a);
-        w[0] = x.x; w[1] = x.y;
-      }
-      __half2 top = *reinterpret_cast<const __half2*>(&w[0]);
-#pragma unroll
-      for (int j = 1; j < W; ++j) top = __hmax2(top, *reinterpret_cast<const __half2*>(&w[j]));
-      most = __low2float(top);
-    }
-#pragma unroll
-    for (int sub0 = 0; sub0 < 2; sub0 += NS) part(tile, j0, flags, special, most, sub0);
-  }
-
-  // Sub-tiles sub0 … sub0 + NS − 1.
-  __device__ __forceinline__ void part(uint32_t tile, int j0, uint32_t flags, bool special, float most, const int sub0) {
-    auto live = [&](int sub, int key) { return ((flags >> sub) & 1u) != 0u && j0 + 16 * sub + key < L; };
-    // ---- scores of keys j0 + 16·sub + g and + 8
+    // ---- scores of keys j0 + 16·ns + g and + 8
     float s[NS][NT][4];
 #pragma unroll
     for (int ns = 0; ns < NS; ++ns) {
-      const int sub = sub0 + ns;
       uint32_t kn[2][W], kp[2][W], mn[2];
-      const uint32_t ak = tile + lane_k + sub * 16 * ROW, ap = tile + lane_p + sub * 16 * PAIR, am = tile + lane_m + sub * 16 * PAIR;
+      const uint32_t ak = tile + lane_k + ns * 16 * ROW, ap = tile + lane_p + ns * 16 * PAIR, am = tile + lane_m + ns * 16 * PAIR;
       if constexpr (W == 4) {
         const uint4 x0 = lds128<0>(ak), x1 = lds128<8 * ROW>(ak), y0 = lds128<0>(ap), y1 = lds128<8 * PAIR>(ap);
         kn[0][0] = x0.x; kn[0][1] = x0.y; kn[0][2] = x0.z; kn[0][3] = x0.w;
@@ -708,6 +698,25 @@ struct Rows4 {
         }
       }
     }
+    // ---- they are divided by 2^e, which is over the largest of them; where the key is not there they become 0 (what the tile
+    // holds may be anything)
+    if (special && !live(lane >> 4, lane & 15)) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j] = 0u;
+    }
+    uint32_t top = w[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int j = 1; j < W; ++j) top = max2<false>(top, w[j] & 0x7fff7fffu);
+    const int e = (int)(max(top & 0xffffu, top >> 16) >> 10) - 14;  // from fp16's exponent: -14 (0 too) … 16
+    const uint32_t down = pack2<false>(__uint_as_float((uint32_t)(127 - e) << 23), __uint_as_float((uint32_t)(127 - e) << 23));
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j] = mul_f16x2(w[j], down);
+    if constexpr (W == 4) st_shared_v4(aw, w[0], w[1], w[2], w[3]);
+    else st_shared_v2(aw, w[0], w[1]);
+    __syncwarp();
+    int ek[NS][2];  // e of keys g, g + 8, g + 16 and g + 24
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ek[i >> 1][i & 1] = __shfl_sync(0xffffffffu, e, g + 8 * i);
     // ---- keys behind a row's last one, or that are not there: they may hold anything, so they are replaced
     if (special || j0 + 31 > L - Nq) {
 #pragma unroll
@@ -716,21 +725,26 @@ struct Rows4 {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int key = g + 8 * (i >> 1), sub = sub0 + ns;
-            if (!live(sub, key) || j0 + 16 * sub + key > lim[nt][i & 1]) s[ns][nt][i] = -INFINITY;
+            const int key = g + 8 * (i >> 1);
+            if (!live(ns, key) || j0 + 16 * ns + key > lim[nt][i & 1]) s[ns][nt][i] = -INFINITY;
           }
     }
+#pragma unroll
+    for (int ns = 0; ns < NS; ++ns)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float x = (float)ek[ns][i >> 1];
+          fma_pair(s[ns][nt][i], s[ns][nt][i + 1], s[ns][nt][i], s[ns][nt][i + 1], coef[nt][0], coef[nt][1], x, x);
+        }
     // ---- the reference (NaN does not raise it: it reaches the sums all the same)
-    bool rise = most > cap_value;
+    bool rise = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-        rise |= top_of(s, nt, u) > rise_at[nt][u];
+      for (int u = 0; u < 2; ++u) rise |= top_of(s, nt, u) > m[nt][u] + (kDepth + kRise);
     if (__any_sync(0xffffffffu, rise)) {
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-      const float next = fmaxf(cap, (float)((int)(__float_as_uint(most) >> 23) - 126));  // 2^next is above it
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -738,12 +752,8 @@ struct Rows4 {
           float x = top_of(s, nt, u);
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-          // m is the reference: 2^(7 − cap) under the largest score when it was set
-          const float r = fmaxf(m[nt][u] + (next - cap), fmaf(x, coef[nt][u], next - kDepth));
-          const float alpha = m[nt][u] == -INFINITY ? 0.f : ex2(m[nt][u] - r);
+          const float r = fmaxf(m[nt][u], x - kDepth), alpha = ex2(m[nt][u] - r);
           m[nt][u] = r;
-          mz[nt][u] = r == -INFINITY ? 0.f : r;
-          rise_at[nt][u] = (r + (kDepth + kRise - next)) / coef[nt][u];
           l[nt][u] *= alpha;
           mins[nt][u] *= alpha;
 #pragma unroll
@@ -752,28 +762,29 @@ struct Rows4 {
             o[nt][j][2 + u] *= alpha;
           }
         }
-      cap = next;
-      cap_value = exp2f(next);
     }
 #pragma unroll
     for (int ns = 0; ns < NS; ++ns) {
-      const int sub = sub0 + ns;
-      // ---- probabilities (up to 2^(15 − cap)), rounded to fp16 and transposed
+      // ---- probabilities times 2^e (up to 2^15), rounded to fp16 and transposed; their sum without that factor
       uint32_t bh[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float pr[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pr[i] = ex2(fmaf(s[ns][nt][i], coef[nt][i & 1], -mz[nt][i & 1]));
-        l[nt][0] += pr[0] + pr[2];
-        l[nt][1] += pr[1] + pr[3];
+        for (int i = 0; i < 4; i += 2) {
+          const float w = __uint_as_float((uint32_t)(127 - ek[ns][i >> 1]) << 23);
+          sub_pair(pr[i], pr[i + 1], s[ns][nt][i], s[ns][nt][i + 1], m[nt][0], m[nt][1]);
+          pr[i] = ex2(pr[i]);
+          pr[i + 1] = ex2(pr[i + 1]);
+          fma_pair(l[nt][0], l[nt][1], pr[i], pr[i + 1], w, w, l[nt][0], l[nt][1]);
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) bh[nt][u] = movmatrix_trans(pack2<false>(pr[2 * u], pr[2 * u + 1]));
       }
       // ---- values of keys 2t, 2t + 1, 2t + 8, 2t + 9: numbers, pairs, and one minimum or scale of each
       uint32_t v[4][W / 2], pair[4][W], one[4];
-      const uint32_t av = tile + lane_v + sub * 16 * ROW, odd = tile + (lane_v ^ ROW) + sub * 16 * ROW;  // row 2t + 1: the swizzle
-      const uint32_t as = tile + lane_s + sub * 16 * PAIR, aa = tile + lane_a + sub * 16 * PAIR;         // turns the row's bit too
+      const uint32_t av = tile + lane_v + ns * 16 * ROW, odd = tile + (lane_v ^ ROW) + ns * 16 * ROW;  // row 2t + 1: the swizzle
+      const uint32_t as = tile + lane_s + ns * 16 * PAIR, aa = tile + lane_a + ns * 16 * PAIR;         // turns the row's bit too
       one[0] = lds16<0>(aa);
       one[1] = lds16<PAIR>(aa);
       one[2] = lds16<8 * PAIR>(aa);
