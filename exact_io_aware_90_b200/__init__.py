@@ -36,7 +36,7 @@ import math
 import os
 from typing import Optional, Tuple
 
-__all__ = [
+_ALL = [  # with the wrappers of paged.py, where they can be had, __all__
     "FAError", "LIB_PATH", "lib", "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA",
     "FA_ERR_TIMEOUT", "FA_BF16", "FA_FP16",
     "fa_fwd", "fa_bwd", "fa_bwd_preprocess", "fa_bwd_main", "fa_bwd_postprocess", "fa_bwd_workspace_bytes",
@@ -45,8 +45,6 @@ __all__ = [
     "FA_CACHE_16BIT", "FA_CACHE_INT4", "fa_rope_table", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
     "fa_qk_norm_rope_bwd_workspace_bytes", "fa_cache_bytes", "fa_cache_append", "fa_cache_gather", "fa_decode_paged",
     "fa_decode_paged_workspace_bytes",
-    "attention_rope_table", "attention_qk_norm_rope", "attention_qk_norm_rope_backward", "attention_cache_append",
-    "attention_cache_gather", "attention_decode_paged",
 ]
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = 0, 1, 2, 3, 4
@@ -488,16 +486,30 @@ def attention_decode(q, k, v, scale: Optional[float] = None, cu_seqlens_k=None, 
     return out, lse
 
 
-
-# The wrappers of paged.py need torch at import; they are loaded on first use, so that the raw ABI does not.
+# The wrappers of paged.py need torch and the binding at import; they are loaded on first use, so that the raw ABI does not.
+# `import *` asks for __all__, which names them where they load: without torch or the binding it brings the rest.
 _PAGED = ("attention_rope_table", "attention_qk_norm_rope", "attention_qk_norm_rope_backward", "attention_cache_append",
           "attention_cache_gather", "attention_decode_paged")
 
 
+def _load_paged():
+    from . import paged
+    for n in _PAGED:
+        globals()[n] = getattr(paged, n)
+
+
 def __getattr__(name):
     if name in _PAGED:
-        from . import paged
-        for n in _PAGED:
-            globals()[n] = getattr(paged, n)
+        _load_paged()
         return globals()[name]
+    if name == "__all__":
+        try:
+            _load_paged()
+        except ImportError:
+            return list(_ALL)
+        return [*_ALL, *_PAGED]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), *_PAGED})

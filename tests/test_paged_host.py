@@ -157,3 +157,30 @@ def test_missing_binding_fails_loudly(fa, tmp_path):
     out = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=300)
     assert out.returncode == 0, out.stderr[-500:]
     assert "sm_100a" in out.stdout and "refused: the torch binding is missing" in out.stdout
+
+
+@pytest.mark.parametrize("torch_found", [True, False])
+def test_star_import_without_the_binding(fa, tmp_path, torch_found):
+    """The raw ABI needs neither the binding nor torch, by `import *` either."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+    pkg = os.path.dirname(fa.__file__)
+    dst = tmp_path / os.path.basename(pkg)
+    os.makedirs(dst)
+    for f in ("__init__.py", "paged.py", "libfa_b200.so"):
+        shutil.copy(os.path.join(pkg, f), dst / f)
+    code = (("" if torch_found else "import sys\nsys.modules['torch'] = None\n")
+            + f"from {dst.name} import *\nprint(fa_version(), attention_forward.__name__, 'attention_decode_paged' in globals())\n")
+    out = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stderr[-500:]
+    assert "sm_100a" in out.stdout and out.stdout.split()[-2:] == ["attention_forward", "False"]
+
+
+def test_star_import_brings_the_wrappers(fa):
+    names = {}
+    exec("from exact_io_aware_90_b200 import *", names)
+    for n in ("attention_rope_table", "attention_qk_norm_rope", "attention_qk_norm_rope_backward", "attention_cache_append",
+              "attention_cache_gather", "attention_decode_paged", "attention_forward", "fa_fwd"):
+        assert names[n] is getattr(fa, n) and n in dir(fa)
