@@ -6,6 +6,7 @@ Both land next to this file; the Python package loads them from there.
 """
 from __future__ import annotations
 
+import json
 import os
 import shutil
 import subprocess
@@ -17,6 +18,7 @@ ROOT = os.path.dirname(HERE)
 LIB_NAME = "libfa_b200.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 BINDING_PATH = os.path.join(HERE, "_binding.so")
+BUILT_FOR_PATH = os.path.join(HERE, "_binding.json")  # the interpreter and torch that _binding.so was built for
 SOURCES = ["libfa_b200.cu"]
 DEPS = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu", "fa_merge.cu", "fa_noalloc.cu", "fa_rope.cu",
         "fa_cache.cu", "fa_paged.cu", "fa_paged_api.cu"]
@@ -41,10 +43,27 @@ def needs_rebuild() -> bool:
     return _older(LIB_PATH, [os.path.join(CSRC, f) for f in SOURCES + DEPS + HEADERS] + [__file__])
 
 
+def _built_for() -> dict:
+    import torch
+    return {"python": sys.version, "torch": str(torch.__version__), "torch_git": str(torch.version.git_version),
+            "cuda": str(torch.version.cuda), "cxx11_abi": int(torch._C._GLIBCXX_USE_CXX11_ABI)}
+
+
+def binding_needs_rebuild() -> bool:
+    """Older than its sources, or built for another interpreter or torch: their C++ ABI differs."""
+    if _older(BINDING_PATH, [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "fa.h"), __file__]):
+        return True
+    try:
+        with open(BUILT_FOR_PATH) as f:
+            return json.load(f) != _built_for()
+    except (OSError, ValueError):
+        return True
+
+
 def build_binding(force: bool = False) -> str:
     """The torch binding: linked against this interpreter's torch and, by a path relative to itself, the library."""
     src = os.path.join(CSRC, "binding.cpp")
-    if not force and not _older(BINDING_PATH, [src, os.path.join(ROOT, "include", "fa.h"), __file__]):
+    if not force and not binding_needs_rebuild():
         return BINDING_PATH
     import sysconfig
 
@@ -64,6 +83,9 @@ def build_binding(force: bool = False) -> str:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError("g++ failed building " + os.path.basename(BINDING_PATH))
     os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+    with open(BUILT_FOR_PATH + ".tmp", "w") as f:
+        json.dump(_built_for(), f)
+    os.replace(BUILT_FOR_PATH + ".tmp", BUILT_FOR_PATH)
     return BINDING_PATH
 
 
