@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -60,14 +61,18 @@ def binding_needs_rebuild() -> bool:
         return True
 
 
-def build_binding(force: bool = False) -> str:
-    """The torch binding: linked against this interpreter's torch and, by a path relative to itself, the library."""
+def build_binding(force: bool = False) -> Optional[str]:
+    """The torch binding: linked against this interpreter's torch and, by a path relative to itself, the library.  Without
+    torch there is none: the library is for use through its C ABI then."""
+    try:
+        import torch
+    except ImportError:
+        sys.stderr.write("torch is not installed: " + os.path.basename(BINDING_PATH) + " (the wrappers of paged.py) is not built\n")
+        return None
+    import sysconfig
     src = os.path.join(CSRC, "binding.cpp")
     if not force and not binding_needs_rebuild():
         return BINDING_PATH
-    import sysconfig
-
-    import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include")

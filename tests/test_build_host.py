@@ -74,3 +74,12 @@ def test_sources_newer_than_their_product(build):
     os.utime(os.path.join(build.CSRC, "fa_rope.cu"), (late, late))
     build.build()
     assert build.ran[3] == "nvcc"
+
+
+def test_library_alone_without_torch(build, monkeypatch, capsys):
+    """The C ABI needs no torch: without it the library is built, and the binding is left out with a word."""
+    monkeypatch.setitem(sys.modules, "torch", None)
+    os.remove(build.LIB_PATH)
+    assert build.build() == build.LIB_PATH and build.ran[2:] == ["nvcc"]
+    assert "torch" in capsys.readouterr().err
+    assert build.build(force=True) == build.LIB_PATH and build.ran[3:] == ["nvcc"]
