@@ -123,6 +123,12 @@ void* flat(const Tensor& t, const char* name, ScalarType dtype, at::IntArrayRef 
   return t.data_ptr();
 }
 
+// A caller's workspace: as many bytes as its elements have, from its address on.  Of a slice with gaps or an expanded tensor
+// that would be memory beside its own.
+void check_workspace(const Tensor* t, at::Device dev) {
+  if (t != nullptr && (t->device() != dev || !t->is_contiguous())) refuse("workspace must be contiguous and on " + dev.str() + ": got " + describe(*t));
+}
+
 // The device made current, and the stream of the call: the given one, else the device's current one.  Memory is
 // allocated on that stream, so that the allocator reuses it in that stream's order.
 struct Place {
@@ -371,7 +377,7 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* args, Py_ssize_t n) 
     const Rows rdk = ok != nullptr ? rows_of(*ok, "dk", dtype, dev, T, d, rgk.heads) : Rows{rgk.heads, rgk.heads * d};
     if (norm && owq != nullptr) flat(*owq, "dwq", at::kFloat, {d}, dev);
     if (norm && owk != nullptr) flat(*owk, "dwk", at::kFloat, {d}, dev);
-    if (ows != nullptr && ows->device() != dev) refuse("workspace must be on the gradients' device");
+    check_workspace(ows, dev);
     const Place at_(a, dev);
     const Tensor dq = oq != nullptr ? *oq : at_.empty({T, rgq.heads, d}, dtype), dk = ok != nullptr ? *ok : at_.empty({T, rgk.heads, d}, dtype);
     Tensor dwq, dwk, ws;
@@ -503,7 +509,7 @@ PyObject* decode_paged(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const auto rows = q.sizes().slice(0, dim - 1);
     if (oo != nullptr) flat(*oo, "out", dtype, q.sizes(), dev);
     if (ol != nullptr) flat(*ol, "lse", at::kFloat, rows, dev);
-    if (ow != nullptr && ow->device() != dev) refuse("workspace must be on q's device");
+    check_workspace(ow, dev);
     const int bound = as_int(Nk, "max_seqlen_k");
     const Place at_(a, dev);
     const Tensor out = oo != nullptr ? *oo : at_.empty(q.sizes(), dtype), lse = ol != nullptr ? *ol : at_.empty(rows, at::kFloat);
