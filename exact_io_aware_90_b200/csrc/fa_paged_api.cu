@@ -218,7 +218,9 @@ int fa_cache_gather(const void* k_cache, const void* v_cache, void* k, void* v, 
 
 static bool paged_sizes(int B, int Nq, int H, int Hk, int Nk, int d) {
   if (B < 1 || Nq < 1 || H < 1 || Hk < 1 || Nk < 1 || (d != 64 && d != 128) || H % Hk != 0) return false;
-  return Nk <= (1 << 30) && H <= (1 << 20) && Nq <= (1 << 20) && (long long)B * Nq * H <= 0x7fffffffLL;
+  if (Nk > (1 << 30) || H > (1 << 20) || Nq > (1 << 20) || (long long)B * Nq * H > 0x7fffffffLL) return false;
+  const long long rows = (long long)(H / Hk) * Nq;
+  return B <= 65535 && rows <= 0x3fffffffLL && (rows + 15) / 16 * Hk <= 65535;  // units in 32 bits
 }
 
 size_t fa_decode_paged_workspace_bytes(int B, int Nq, int H, int Hk, int Nk, int d) {
@@ -237,8 +239,6 @@ int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, voi
   if (!aligned16(q) || !aligned16(o) || !aligned4(lse)) return FA_ERR_INVALID_ARG;
   if (Nq < 1 || H < 1 || Nk < 1 || H % Hk != 0 || !std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
   if (!paged_sizes(B, Nq, H, Hk, Nk, d)) return FA_ERR_UNSUPPORTED;
-  const long long rows = (long long)(H / Hk) * Nq;
-  if (B > 65535 || rows > 0x3fffffffLL || (rows + 15) / 16 * Hk > 65535) return FA_ERR_UNSUPPORTED;  // units in 32 bits
   size_t ml_at, units_at;
   const size_t need = decode_paged_workspace(B, Nq, H, Hk, Nk, d, &ml_at, &units_at);
   if (need > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes_ < need))

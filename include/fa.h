@@ -499,6 +499,7 @@ int fa_cache_gather(const void* k_cache, const void* v_cache, void* k, void* v, 
  * is 0: small calls need none.  A sequence whose length is out of range is skipped,
  * its rows of o and lse left as they are.
  */
+/* 0 too for sizes that fa_decode_paged refuses. */
 size_t fa_decode_paged_workspace_bytes(int B, int Nq, int H, int Hk, int Nk, int d);
 int fa_decode_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
                     const int32_t* page_table, const int32_t* seqlens_k, int B, int Nq, int H, int Hk, int Nk, int d,

@@ -184,3 +184,13 @@ def test_star_import_brings_the_wrappers(fa):
     for n in ("attention_rope_table", "attention_qk_norm_rope", "attention_qk_norm_rope_backward", "attention_cache_append",
               "attention_cache_gather", "attention_decode_paged", "attention_forward", "fa_fwd"):
         assert names[n] is getattr(fa, n) and n in dir(fa)
+
+
+def test_decode_workspace_of_sizes_that_are_refused(fa):
+    """No size for what fa_decode_paged refuses; with 2^31 - 2 rows the row tiles passed 32 bits and gave 5.7 TB."""
+    good = dict(q=P16, k_cache=P16, v_cache=P16, o=P16, lse=P16, page_table=P16, seqlens_k=P16, num_pages=3, max_pages=2, scale=0.125,
+                page_size=16, dtype=0, cache_format=0, workspace=P16, workspace_bytes=1 << 50, stream=None)
+    for B, Nq, H, Hk in ((1, 3906, 549791, 1), (65536, 1, 1, 1), (1, 1 << 20, 1 << 10, 1), (1, 1, 1 << 17, 1 << 17), (1, 1 << 20, 16, 16)):
+        assert fa.fa_decode_paged_workspace_bytes(B, Nq, H, Hk, 100000, 64) == 0
+        assert fa.fa_decode_paged(**dict(good, B=B, Nq=Nq, H=H, Hk=Hk, Nk=100000, d=64)) == fa.FA_ERR_UNSUPPORTED
+    assert fa.fa_decode_paged_workspace_bytes(65535, 1, 16, 16, 100000, 64) > 0
