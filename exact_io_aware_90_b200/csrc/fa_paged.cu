@@ -611,7 +611,8 @@ struct Rows4 {
       // k-index 0-3: the first parts of groups 0-3, 4-7: the second parts
       qs[nt] = t == 0 ? pack2<false>(hi[0], hi[1]) : t == 1 ? pack2<false>(hi[2], hi[3])
              : t == 2 ? pack2<false>(lo[0], lo[1]) : pack2<false>(lo[2], lo[3]);
-      const float back = __uint_as_float((uint32_t)(127 + 12 + e) << 23) * p.scale_log2;
+      // at least the smallest normal number: a factor of 0 would make a masked score of -inf NaN
+      const float back = fmaxf(__uint_as_float((uint32_t)(127 + 12 + e) << 23) * p.scale_log2, 1.17549435e-38f);
       coef[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
       coef[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
 #pragma unroll

@@ -107,3 +107,30 @@ def test_one_large_value_without_weight(fa, at, first, size, dtype, heads, most)
     values[first] = 0.0
     values[at] = np.linspace(-7.5, 7.5, d) * size
     _check(fa, scores, values, dtype, heads, most)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("scale", [1e-25, 1e-37])
+def test_queries_and_scales_near_zero(fa, scale, dtype):
+    """Scores that are 0 to every digit: the mean of the values that a row sees, whatever the tile's places behind the sequence
+    hold.  Errors as above: 2^-11 of each value and, for bf16 outputs, of 8·scale, 2^-16 of n·scale + |min|, the output's own."""
+    n, d = 37, 64
+    g = torch.Generator().manual_seed(5)
+    k, v = (torch.randn(1, 1, PAGE, d, generator=g).to(DT[dtype]) for _ in range(2))
+    caches = [torch.from_numpy(oracle.four_bit_pack(*oracle.four_bit_rows(f64(x)), i == 1)).reshape(1, 1, PAGE, d * 5 // 8)
+              for i, x in enumerate((k, v))]
+    table = np.zeros((1, 1), np.int32)
+    vr, va, vm, vs = (x[:, 0] for x in oracle.cache_rows(caches[1], table, 0, np.arange(n), d, True))
+    q = torch.zeros(1, 2, 3, d, dtype=DT[dtype])
+    q[0, :, 1] = 1.0
+    q[0, :, 2, 0] = 2.0 ** -20
+    for most in (None, 100000):
+        o, lse = fa.attention_decode_paged(q.cuda(), *(x.cuda() for x in caches), torch.from_numpy(table).cuda(),
+                                           torch.tensor([n], dtype=torch.int32).cuda(), max_seqlen_k=most, scale=scale)
+        assert fa.fa_check_device_status(torch.cuda.current_stream().cuda_stream) == fa.FA_OK
+        u = torch.finfo(DT[dtype]).eps / 2
+        for i, m in enumerate((n - 1, n)):
+            ref = vr[:m].mean(0)
+            bound = (np.abs(vr) * 2.0 ** -11 + 8 * vs * (2.0 ** -11 if dtype == "bf16" else 0) + (np.abs(va) + np.abs(vm)) * 2.0 ** -16)[:m].mean(0)
+            bound = bound + u * np.abs(ref) * (1 + 2.0 ** -7) + 2.0 ** -25
+            assert np.all(np.abs(f64(o)[0, i] - ref) <= bound) and np.all(np.abs(f64(lse)[0, i] - np.log(m)) <= 2.0 ** -18)
