@@ -74,8 +74,9 @@ constexpr float kRise = 8.f;  // how far a score may pass the reference before t
 // Blocks per SM of a variant.
 constexpr int paged_blocks(int d, bool q4, int nt) { return d == 64 ? (nt == 2 ? 3 : 4) : nt == 2 || !q4 ? 2 : 3; }
 
-// Tile and ring depth of a variant: at least 40 KB in flight per SM (HBM latency times its share of the
-// bandwidth), within 227 KB of shared memory and the registers.
+// Tile and ring depth of a variant: what all warps have in flight per SM is 96 to 128 KB in 16 bits and 40 to 60 KB in 4 bits
+// (30 KB at d = 64 with two row tiles), against some 40 KB for HBM's latency times an SM's share of the bandwidth; within 227 KB
+// of shared memory and the registers.
 template <int D, bool Q4, int NT>
 struct PagedConfig {
   static constexpr int kTile = Q4 ? 32 : 16;             // keys of a warp's tile
@@ -889,87 +890,87 @@ __device__ __forceinline__ void run_piece(const PagedParams& p, uint8_t* smem, i
   const bool paired = Q4 && ps % 32 != 0;  // a tile's two halves may lie in two pages
   const int step_pages = GK / ps, step_slots = GK - step_pages * ps;
 
-      // ---- the warp's tiles, keys GK·i + T·warp on; page lookups run one tile ahead of the copies
-      const int32_t* table = p.pg.page_table + (size_t)b * p.pg.max_pages;
-      const int tiles = last - first - (GK * (last - 1) + T * warp >= L ? 1 : 0);
-      const TileCopy<D, Q4> copy(p.pg, hk, ring, lane);
-      int next_j = GK * first + T * warp;  // the first key of the next tile to be copied
-      int page_i = next_j / ps, slot = next_j - page_i * ps;
-      int page = tiles > 0 ? load_now(table + page_i) : 0, page2 = 0;
-      auto second = [&]() { return slot + 16 >= ps ? page_i + 1 : page_i; };  // the second half's page index
-      if (paired && tiles > 0 && next_j + 16 < L) page2 = load_now(table + second());
-      int left = tiles;      // to be copied
-      uint32_t copy_at = 0;  // the stage of the next one
-      uint32_t valid = 0;    // two bits for each of the last tiles copied: the halves that are there
-      auto issue = [&]() {
-        valid *= 4;
-        if (left > 0) {
-          --left;
-          const bool ok = (unsigned)page < (unsigned)p.pg.num_pages;
-          bool bad = !ok;
-          if (!paired) {
-            if (ok) copy.template rows<T / 16>(page, slot, copy_at, 0);
-            valid += ok ? 3u : 0u;
-          } else {
-            if (ok) copy.template rows<1>(page, slot, copy_at, 0);
-            valid += ok ? 1u : 0u;
-            if (next_j + 16 < L) {
-              const bool ok2 = (unsigned)page2 < (unsigned)p.pg.num_pages;
-              if (ok2) copy.template rows<1>(page2, slot + 16 >= ps ? slot + 16 - ps : slot + 16, copy_at, 1);
-              valid += ok2 ? 2u : 0u;
-              bad = bad || !ok2;
-            }
-          }
-          if (bad && lane == 0) record_status(1);
-          next_j += GK;
-          page_i += step_pages;
-          slot += step_slots;
-          if (slot >= ps) {
-            slot -= ps;
-            ++page_i;
-          }
-          if (left > 0) {
-            page = load_now(table + page_i);
-            if (paired && next_j + 16 < L) page2 = load_now(table + second());
-          }
+  // ---- the warp's tiles, keys GK·i + T·warp on; page lookups run one tile ahead of the copies
+  const int32_t* table = p.pg.page_table + (size_t)b * p.pg.max_pages;
+  const int tiles = last - first - (GK * (last - 1) + T * warp >= L ? 1 : 0);
+  const TileCopy<D, Q4> copy(p.pg, hk, ring, lane);
+  int next_j = GK * first + T * warp;  // the first key of the next tile to be copied
+  int page_i = next_j / ps, slot = next_j - page_i * ps;
+  int page = tiles > 0 ? load_now(table + page_i) : 0, page2 = 0;
+  auto second = [&]() { return slot + 16 >= ps ? page_i + 1 : page_i; };  // the second half's page index
+  if (paired && tiles > 0 && next_j + 16 < L) page2 = load_now(table + second());
+  int left = tiles;      // to be copied
+  uint32_t copy_at = 0;  // the stage of the next one
+  uint32_t valid = 0;    // two bits for each of the last tiles copied: the halves that are there
+  auto issue = [&]() {
+    valid *= 4;
+    if (left > 0) {
+      --left;
+      const bool ok = (unsigned)page < (unsigned)p.pg.num_pages;
+      bool bad = !ok;
+      if (!paired) {
+        if (ok) copy.template rows<T / 16>(page, slot, copy_at, 0);
+        valid += ok ? 3u : 0u;
+      } else {
+        if (ok) copy.template rows<1>(page, slot, copy_at, 0);
+        valid += ok ? 1u : 0u;
+        if (next_j + 16 < L) {
+          const bool ok2 = (unsigned)page2 < (unsigned)p.pg.num_pages;
+          if (ok2) copy.template rows<1>(page2, slot + 16 >= ps ? slot + 16 - ps : slot + 16, copy_at, 1);
+          valid += ok2 ? 2u : 0u;
+          bad = bad || !ok2;
         }
-        copy_at = copy_at == (S - 1) * Cfg::kTileBytes ? 0 : copy_at + Cfg::kTileBytes;
-        cp_async_commit();
-      };
-  #pragma unroll
-      for (int s = 0; s < S - 1; ++s) issue();
-
-      Rows rows;
-      rows.init(p, b, hk, r0, L, lane);
-      uint32_t tile = ring + (S - 1) * Cfg::kTileBytes;
-      int j0 = GK * (first - 1) + T * warp;
-  #pragma unroll 1
-      for (int it = 0; it < tiles; ++it) {
-        cp_async_wait<S - 2>();
-        __syncwarp();  // the tile is here for every lane, and every lane is done with the one before
-        const uint32_t flags = (valid >> (2 * (S - 2))) & 3u;
-        issue();
-        tile = tile == ring + (S - 1) * Cfg::kTileBytes ? ring : tile + Cfg::kTileBytes;
-        j0 += GK;
-        if (flags != 0u) rows.step(tile, j0, flags);
       }
-      cp_async_wait<0>();
-      __syncthreads();  // every warp is done with its ring: the memory now holds the warps' partial outputs
-  #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-  #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int r = 8 * nt + 2 * (lane & 3) + u;
-          float x = rows.l[nt][u];
-  #pragma unroll
-          for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-          if (lane < 4) {
-            s_m[warp][r] = rows.m[nt][u];
-            s_l[warp][r] = x;
-          }
-          rows.store(s_o + (warp * ROWS + r) * Cfg::kPitch, nt, u);
-        }
-      __syncthreads();
+      if (bad && lane == 0) record_status(1);
+      next_j += GK;
+      page_i += step_pages;
+      slot += step_slots;
+      if (slot >= ps) {
+        slot -= ps;
+        ++page_i;
+      }
+      if (left > 0) {
+        page = load_now(table + page_i);
+        if (paired && next_j + 16 < L) page2 = load_now(table + second());
+      }
+    }
+    copy_at = copy_at == (S - 1) * Cfg::kTileBytes ? 0 : copy_at + Cfg::kTileBytes;
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) issue();
+
+  Rows rows;
+  rows.init(p, b, hk, r0, L, lane);
+  uint32_t tile = ring + (S - 1) * Cfg::kTileBytes;
+  int j0 = GK * (first - 1) + T * warp;
+#pragma unroll 1
+  for (int it = 0; it < tiles; ++it) {
+    cp_async_wait<S - 2>();
+    __syncwarp();  // the tile is here for every lane, and every lane is done with the one before
+    const uint32_t flags = (valid >> (2 * (S - 2))) & 3u;
+    issue();
+    tile = tile == ring + (S - 1) * Cfg::kTileBytes ? ring : tile + Cfg::kTileBytes;
+    j0 += GK;
+    if (flags != 0u) rows.step(tile, j0, flags);
+  }
+  cp_async_wait<0>();
+  __syncthreads();  // every warp is done with its ring: the memory now holds the warps' partial outputs
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = 8 * nt + 2 * (lane & 3) + u;
+      float x = rows.l[nt][u];
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+      if (lane < 4) {
+        s_m[warp][r] = rows.m[nt][u];
+        s_l[warp][r] = x;
+      }
+      rows.store(s_o + (warp * ROWS + r) * Cfg::kPitch, nt, u);
+    }
+  __syncthreads();
   // ---- the block's: a warp per row, d/32 features per lane
 #pragma unroll 1
   for (int r = warp; r < ROWS && r0 + r < p.R; r += kPagedWarps) {

@@ -20,7 +20,7 @@
 namespace fa {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeStages = 4;  // of the backward's ring: 80 KB in flight per block, two blocks per SM
+constexpr int kRopeStages = 4;  // of the backward's ring: 64 KB per block, three stages (48 KB) in flight; two blocks per SM
 constexpr int kRopeRing = kRopeThreads / 32 * kRopeStages * 4 * 32 * 16;
 
 // ---------------------------------------------------------------- table

@@ -492,7 +492,8 @@ int fa_cache_gather(const void* k_cache, const void* v_cache, void* k, void* v, 
  * of o infinite or NaN.  (4 bits: the scales and minima of the sequence's keys are
  * finite, as fa_cache_append leaves them.)
  * The scores and sums are fp32; P carries two 16-bit parts into the product with
- * V (4-bit cache: one fp16 part of P times the value's scale).  The workspace
+ * V (4-bit cache: P is rounded to fp16 once, and its product with the value's
+ * scale again in bf16; in fp16 that product carries a second part).  The workspace
  * holds the parts of runs of keys; a 256-byte aligned buffer of
  * fa_decode_paged_workspace_bytes(...) bytes, contents irrelevant (calls that may run at
  * the same time need one each), or NULL where that
