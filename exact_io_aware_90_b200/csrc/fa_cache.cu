@@ -8,8 +8,9 @@
 // row is made from the row rounded to 16 bits — what the 16-bit cache would hold — so that both formats
 // start from the same values.
 // Measured, bf16, d = 128: append of 31.6k tokens of 32 + 8 + 8 heads, 16 bits 776 MB in 136 us (87 % of the measured copy
-// bandwidth), 4 bits 173 us: instructions bound it there (325 per 512/d rows on average, 64 % of the issue slots: the
-// minimum, maximum and rounding of a 4-bit row cost twice its norm and rotation).  Gather of 16 x 8192 keys of 8 heads,
+// bandwidth), 4 bits 185 us: instructions bound it there (325 per 512/d rows on average, 64 % of the issue slots: the
+// minimum, maximum and rounding of a 4-bit row cost twice its norm and rotation; held to 80 registers for three blocks a
+// multiprocessor, a thread spills 100 bytes in 4 bits and 28 to 56 in 16, and warps wait for instructions).  Gather of 16 x 8192 keys of 8 heads,
 // 16 bits 162 us (101 %), 4 bits 705 MB in 119 us (90 %).  16 tokens appended: 2.9 us, the launch and the chain of lookups.
 // A ring of asynchronous copies, as in the norm's gradient, was no faster here: 139 us in 16 bits, and 4 bits the same.
 #include "paged.cuh"

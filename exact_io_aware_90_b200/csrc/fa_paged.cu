@@ -28,17 +28,18 @@
 // A lane's scores and outputs belong to the same two rows (2t, 2t+1), so rescaling needs no exchange either.
 // The pieces are written to shared memory at places that keep these reads free of bank conflicts.
 //
-// Measured, d = 128: 16 x 8192 keys of 16 heads in 16 bits 1074 MB in 164 us (100 % of the measured copy bandwidth);
-// 64 sequences of 512 to 16384 keys, 8 key heads, 4 query heads each, in 4 bits 743 MB in 162 us (70 %); 131071 keys of 8
-// heads, 16 query rows, fp16, in 4 bits 168 MB in 70 us (37 %); one sequence of 777 keys and 16 heads 6.1 us (the launch and
-// a chain of lookups and copies).
+// Measured, d = 128: 16 x 8192 keys of 16 heads in 16 bits 1074 MB in 165 to 169 us (97 to 99 % of the measured copy
+// bandwidth); 64 sequences of 512 to 16384 keys, 8 key heads, 4 query heads each, in 4 bits 744 MB in 167 us (68 %); 131071
+// keys of 8 heads, 16 query rows, fp16, in 4 bits 168 MB in 72 us (35 %); one sequence of 777 keys and 16 heads 6.2 us (the
+// launch and a chain of lookups and copies).  Over 16 rows a key head, each tile of 16 reads the keys again, from HBM where
+// they do not fit L2: 1074 MB of 16-bit keys and values with 16, 32 and 60 rows 1.08, 2.15 and 4.28 GB, 181, 343 and 659 us.
 //
 // The reference of the exponents rises only when a score passes it by 2^8 (one vote per tile).  P of 16-bit caches is
 // the sum of two 16-bit parts, so its rounding stays behind the output's; in fp16 the reference is 2^7 below the maximum,
 // so that P, up to 2^15, keeps keys down to 2^-32 of the largest (many of them may outweigh it).
 //
 // 4 bits.  Instructions bound this path (16 keys by 8 rows of d = 128 have 2,560 bytes to read and 4,096 numbers to unpack;
-// 347 instructions per warp, 52 % of the issue slots with three warps per scheduler, the integer pipe 45 % busy, HBM 70 %),
+// 362 instructions per warp, 52 % of the issue slots with three warps per scheduler, the integer pipe 46 % busy, HBM 68 %),
 // so everything is arranged to keep their number low; the first arrangement, the plain formula, took 603:
 //   * Numbers are used where they lie: a masked half word with n in bits 0-3 is the fp16 n·2^-24, with n in bits 4-7
 //     n·2^-20 (subnormal, and exact in the products).  The queries are taken to fp16 by a power of two per row that

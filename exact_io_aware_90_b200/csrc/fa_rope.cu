@@ -2,8 +2,8 @@
 // position in one pass, its gradient, and the table of angles (see rope.cuh for the row arithmetic).
 //
 // Streams of a few fp32 operations per value read and written, bound by HBM bandwidth where there are many tokens
-// (32768 tokens of 16 + 16 heads, d = 128, bf16: forward 541 MB in 91 us, gradient 810 MB in 130 us, 91 and 95 % of the
-// measured copy bandwidth) and by the launch where there are few.
+// (32768 tokens of 16 + 16 heads, d = 128, bf16: forward 541 MB in 91 us, gradient 810 MB in 132 us, 91 and 94 % of the
+// measured copy bandwidth; under the power cap of long runs 93 and 142) and by the launch where there are few.
 //
 //   fa_qk_norm_rope_kernel      a warp takes one token: its cos and sin are loaded once and serve every
 //                               head; 512/d rows at a time, 16-byte loads and stores

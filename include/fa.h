@@ -467,7 +467,8 @@ int fa_cache_append(const void* q, const void* k, const void* v, void* q_out, vo
 
 /*
  * Reads rows of a paged cache back into packed k, v [total_keys, Hk, d] of the
- * dtype (what fa_fwd and fa_decode read): row cu_seqlens_k[b] + i is position
+ * dtype (the layout of fa_fwd and fa_decode, which take as many key heads as
+ * query heads, and fa_fwd as many keys as queries): row cu_seqlens_k[b] + i is position
  * starts[b] + i of sequence b (starts NULL: 0; cu_seqlens_k NULL: total_keys/B
  * rows each).  4-bit rows come as n·scale + min, rounded once.  Rows that belong
  * to no sequence are left as they are.
