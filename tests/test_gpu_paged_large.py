@@ -59,8 +59,6 @@ def _pages(lens, page, rng):
                                                    (64, 0, 17, 32, 48, True), (128, 0, 9, 64, 128, False), (64, 3, 5, 16, 0, False),
                                                    (128, 16, 16, 32, 0, True)])
 def test_append(fa, d, hq, hk, page, rot, norm, inter, dtype, bits, tokens):
-    if rot == 0 and inter:
-        pytest.skip("no pairs without rotation")
     rng = np.random.default_rng(tokens + hq + 31 * hk + d)
     new = _ragged(tokens - 3, 23, rng)                   # three rows behind the last sequence
     lens = new + rng.integers(0, 40, len(new))
@@ -75,7 +73,7 @@ def test_append(fa, d, hq, hk, page, rot, norm, inter, dtype, bits, tokens):
     kc, vc = (x.cuda() if bits == 4 else x.cuda().view(DT[dtype]) for x in before)
     qo = torch.full((tokens, hq, d), 9.0, dtype=DT[dtype], device="cuda") if hq else None
     cu = torch.from_numpy(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)).cuda()
-    turn = dict(cos=cos, sin=sin, interleaved=inter) if rot else {}
+    turn = dict(interleaved=inter, **(dict(cos=cos, sin=sin) if rot else {}))
     weights = dict(wq=wq if hq else None, wk=wk) if norm else {}
     got = fa.attention_cache_append(k, v, kc, vc, torch.from_numpy(table).cuda(), torch.from_numpy(lens.astype(np.int32)).cuda(), q=q if hq else None,
                                     eps=EPS, cu_seqlens=cu, q_out=qo, **turn, **weights)
